@@ -32,6 +32,7 @@ DSPARK_DEV_BAD_LENGTH = 2
 DSPARK_DEV_WAIT_TIMEOUT = 4
 DSPARK_DEV_CAPACITY = 8
 DSPARK_DEV_RANGE = 16
+DSPARK_DEV_BAD_PAGE = 32
 DSPARK_DTYPE_F32 = 0
 DSPARK_DTYPE_BF16 = 1
 DSPARK_DTYPE_F16 = 2
@@ -71,6 +72,12 @@ class dspark_kv_cache(ctypes.Structure):
                 ("capacity", c_i32), ("pos0", c_i32p)]
 
 
+class dspark_paged_cache(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("block_table", c_vp), ("status", c_vp)] + \
+        [(n, c_i32) for n in ("layers", "num_pages", "page_size", "n_kv", "head_dim", "batch", "max_pages", "dtype")]
+
+
+c_i64 = ctypes.c_int64
 _PROTOTYPES = {
     "dspark_kv_dtype": (c_i32, [ctypes.POINTER(dspark_config)]),
     "dspark_model_workspace_bytes": (c_size, [ctypes.POINTER(dspark_config)]),
@@ -92,6 +99,16 @@ _PROTOTYPES = {
                               c_size, c_vp]),
     "dspark_attend_no_alloc": (c_i32, [c_vp, c_i32, ctypes.POINTER(dspark_kv_cache), c_vp, c_vp, c_vp, c_vp, c_i32,
                                        c_i32, c_vp]),
+    "dspark_page_slots": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                  c_vp, c_vp]),
+    "dspark_norm_rope_paged": (c_i32, [c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp,
+                                       c_f32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "dspark_attend_paged_workspace_bytes": (c_size, [c_vp, c_i32, c_i32, c_i32]),
+    "dspark_attend_paged": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_f32, c_i32, c_i32,
+                                    c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    "dspark_sample_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "dspark_sample": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
+                              c_vp]),
     "dspark_debug_attention_dump": (c_i32, [c_vp, c_vp, c_size]),
     "dspark_debug_logit_stats": (c_i32, [c_vp, c_vp, c_size]),
     "dspark_debug_wait_probe": (c_i32, [c_vp, c_i32, c_vp]),
@@ -223,6 +240,240 @@ def prune_lengths(conf, thresholds, lengths=None, stream=None):
     _check(get_lib().dspark_prune_lengths(conf.data_ptr(), A, gamma, thresholds.data_ptr(), lengths.data_ptr(),
                                           _stream_ptr(stream)))
     return lengths
+
+
+# ---------------------------------------------------------------- the paged verification step
+_DTYPE_CODES = {}
+
+
+def _dtype_code(dtype) -> int:
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float32: DSPARK_DTYPE_F32, torch.bfloat16: DSPARK_DTYPE_BF16, torch.float16: DSPARK_DTYPE_F16})
+    try:
+        return _DTYPE_CODES[dtype]
+    except KeyError:
+        raise DsparkError(DSPARK_ERR_INVALID_ARGUMENT, f"dtype {dtype} is not fp32, bf16 or fp16") from None
+
+
+def _refuse(msg: str):
+    raise DsparkError(DSPARK_ERR_INVALID_ARGUMENT, msg)
+
+
+def _vec(t, name: str, dtype, n: int, dev: int):
+    """Checks a contiguous 1-d device array of at least n entries; returns its address."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(f"{name} must be a contiguous {dtype} tensor of at least {n} entries on cuda:{dev}")
+    return t.data_ptr()
+
+
+class _on:
+    """Makes the tensors' device current around a call when it is not, and gives the stream's address."""
+    __slots__ = ("dev", "stream", "prev")
+
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.prev = dev, stream, None
+
+    def __enter__(self):
+        import torch
+        cur = torch.cuda.current_device()
+        if cur != self.dev:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            import torch
+            torch.cuda.set_device(self.prev)
+
+
+class PagedKvCache:
+    """A paged K/V cache (``dspark_paged_cache``): k, v [layers, num_pages, page_size, n_kv, head_dim]
+    and the block table int32 [batch, max_pages] that the layers share, all on one CUDA device.
+
+    ``k``, ``v`` and ``block_table`` may be given (the caller's tensors, which must stay alive and in
+    place) or are allocated: ``batch`` and ``max_pages`` then size the table (-1 throughout).
+    ``read_status()`` returns and clears the ``DSPARK_DEV_*`` bits the kernels recorded."""
+
+    def __init__(self, num_pages: int, page_size: int, n_kv: int, head_dim: int, block_table=None, batch: int = 0,
+                 max_pages: int = 0, layers: int = 1, dtype=None, device="cuda", k=None, v=None):
+        import torch
+        if (k is None) != (v is None):
+            _refuse("give both k and v, or neither")
+        if k is None:
+            shape = (layers, num_pages, page_size, n_kv, head_dim)
+            k, v = (torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2))
+        for name, t in (("k", k), ("v", v)):
+            if tuple(t.shape[1:]) != (num_pages, page_size, n_kv, head_dim) or t.dim() != 5 or not t.is_contiguous() or not t.is_cuda:
+                _refuse(f"{name} must be a contiguous CUDA tensor [layers, num_pages, page_size, n_kv, head_dim]")
+        if v.shape != k.shape or v.dtype is not k.dtype or v.device != k.device:
+            _refuse("k and v must have the same shape, dtype and device")
+        if block_table is None:
+            block_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=k.device)
+        if block_table.dtype is not torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous() or \
+                block_table.device != k.device:
+            _refuse("block_table must be a contiguous int32 tensor [batch, max_pages] on the cache's device")
+        self.k, self.v, self.block_table = k, v, block_table
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.device, self.dev, self.dtype = k.device, k.get_device(), k.dtype
+        self.layers, self.num_pages, self.page_size, self.n_kv, self.head_dim = (int(x) for x in k.shape)
+        self.batch, self.max_pages = (int(x) for x in block_table.shape)
+        st = dspark_paged_cache()
+        st.k, st.v, st.block_table, st.status = k.data_ptr(), v.data_ptr(), block_table.data_ptr(), self.status.data_ptr()
+        for n in ("layers", "num_pages", "page_size", "n_kv", "head_dim", "batch", "max_pages"):
+            setattr(st, n, getattr(self, n))
+        st.dtype = _dtype_code(k.dtype)
+        self.struct = st
+        self.ref = ctypes.addressof(st)
+
+    def read_status(self) -> int:
+        v = int(self.status.item())
+        if v:
+            self.status.zero_()
+        return v
+
+
+def page_slots(cache: PagedKvCache, ctx_len, n_new, n_pages, free_pages, free_count, max_tokens: int, n_pages_out=None,
+               free_count_out=None, cu_new=None, kv_len=None, slots=None, positions=None, stream=None):
+    """Pages, block table rows, slots and positions of a step's new tokens from lengths on the device
+    (``dspark_page_slots``). ``ctx_len``, ``n_new``, ``n_pages`` int32 [B]; ``free_pages`` int32 [n_free],
+    ``free_count`` int32 [1]. Missing outputs are allocated (n_pages_out = n_pages and the like update in
+    place); returns (cu_new, kv_len, slots, positions, n_pages_out, free_count_out)."""
+    import torch
+    i32, B, dev = torch.int32, ctx_len.shape[0], cache.dev
+    new = lambda n, dt=i32: torch.empty(n, dtype=dt, device=cache.device)  # noqa: E731
+    n_pages_out = new(B) if n_pages_out is None else n_pages_out
+    free_count_out = new(1) if free_count_out is None else free_count_out
+    cu_new = new(B + 1) if cu_new is None else cu_new
+    kv_len = new(B) if kv_len is None else kv_len
+    slots = new(max_tokens, torch.int64) if slots is None else slots
+    positions = new(max_tokens) if positions is None else positions
+    with _on(dev, stream) as s:
+        _check(get_lib().dspark_page_slots(
+            cache.ref, _vec(ctx_len, "ctx_len", i32, B, dev), _vec(n_new, "n_new", i32, B, dev), B,
+            _vec(n_pages, "n_pages", i32, B, dev), _vec(free_pages, "free_pages", i32, 0, dev), free_pages.shape[0],
+            _vec(free_count, "free_count", i32, 1, dev), max_tokens, _vec(n_pages_out, "n_pages_out", i32, B, dev),
+            _vec(free_count_out, "free_count_out", i32, 1, dev), _vec(cu_new, "cu_new", i32, B + 1, dev),
+            _vec(kv_len, "kv_len", i32, B, dev), _vec(slots, "slots", torch.int64, max_tokens, dev),
+            _vec(positions, "positions", i32, max_tokens, dev), s))
+    return cu_new, kv_len, slots, positions, n_pages_out, free_count_out
+
+
+def _heads(t, name: str, n_heads: Optional[int], hd: int, dev: int):
+    """Checks [T, heads, hd] with contiguous heads on the device; returns the token stride."""
+    if t.dim() != 3 or t.shape[2] != hd or (n_heads is not None and t.shape[1] != n_heads) or t.get_device() != dev or \
+            t.stride(2) != 1 or (t.stride(1) != hd and t.shape[1] > 1):
+        _refuse(f"{name} must be [T, heads, {hd}] on cuda:{dev} with contiguous heads" +
+                (f" ({n_heads} of them)" if n_heads is not None else ""))
+    return t.stride(0)
+
+
+def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: PagedKvCache, layer: int, eps: float = 1e-6,
+                    v_norm: bool = False, q_out=None, stream=None):
+    """RMS norms of the q and k heads, their rotation and the write of k and v into the pages
+    (``dspark_norm_rope_paged``). ``q`` [T, nH, hd], ``k``, ``v`` [T, nKv, hd] may be slices of one product
+    (any token stride); ``v`` None takes the values from ``k``. ``inv_freq`` float64 [hd / 2] (see
+    ``rope_inv_freq``); ``positions`` int32 [T], ``slots`` int64 [T] (negative: a padding row, left alone).
+    Returns q_out [T, nH, hd] in the cache's dtype."""
+    import torch
+    hd, dev, T, nH = cache.head_dim, cache.dev, q.shape[0], q.shape[1]
+    qs, ks = _heads(q, "q", None, hd, dev), _heads(k, "k", cache.n_kv, hd, dev)
+    vs = _heads(v, "v", cache.n_kv, hd, dev) if v is not None else 0
+    dt = q.dtype
+    if k.dtype is not dt or k.shape[0] < T or (v is not None and (v.dtype is not dt or v.shape[0] < T)):
+        _refuse("q, k and v must have one dtype and the same tokens")
+    if q_out is None:
+        q_out = torch.empty(T, nH, hd, dtype=cache.dtype, device=cache.device)
+    elif q_out.dtype is not cache.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != dev:
+        _refuse("q_out must be a contiguous [T, heads, head_dim] tensor in the cache's dtype")
+    with _on(dev, stream) as s:
+        _check(get_lib().dspark_norm_rope_paged(
+            cache.ref, layer, _dtype_code(dt), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, nH,
+            _vec(q_norm, "q_norm", dt, hd, dev) if q_norm is not None else None,
+            _vec(k_norm, "k_norm", dt, hd, dev) if k_norm is not None else None,
+            _vec(inv_freq, "inv_freq", torch.float64, hd // 2, dev), eps, 1 if v_norm else 0,
+            _vec(positions, "positions", torch.int32, T, dev), _vec(slots, "slots", torch.int64, T, dev), T,
+            q_out.data_ptr(), s))
+    return q_out
+
+
+def rope_inv_freq(head_dim: int, theta: float = 1e6, partial_rotary_factor: float = 1.0, device="cuda"):
+    """The proportional RoPE table [head_dim / 2] in float64: theta^(-2i / head_dim) for the first
+    floor(head_dim * partial) / 2 pairs, 0 (identity) for the rest."""
+    import torch
+    i = torch.arange(head_dim // 2, dtype=torch.float64)
+    f = float(theta) ** (-2.0 * i / head_dim)
+    f[int(head_dim * partial_rotary_factor) // 2:] = 0.0
+    return f.to(device)
+
+
+def attend_paged_workspace(cache: PagedKvCache, T: int, n_heads: int, B: int):
+    """A workspace for ``attend_paged`` calls of up to T tokens and B requests."""
+    import torch
+    n = get_lib().dspark_attend_paged_workspace_bytes(cache.ref, T, n_heads, B)
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=cache.device)
+
+
+def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: int, scale: float, causal: bool = True,
+                 window: int = 0, out=None, lse=None, ws=None, stream=None):
+    """Attention of each request's new tokens over its pages (``dspark_attend_paged``). ``q`` [T, nH, hd] in
+    the cache's dtype (any token stride), ``cu_new`` int32 [B + 1], ``kv_len`` int32 [B] as ``page_slots``
+    gives them, ``max_new`` the most new tokens of a request. Returns out [T, nH, hd]; ``lse`` float32
+    [T, nH] is filled if given."""
+    import torch
+    dev, T, nH, B = cache.dev, q.shape[0], q.shape[1], kv_len.shape[0]
+    qs = _heads(q, "q", None, cache.head_dim, dev)
+    if q.dtype is not cache.dtype:
+        _refuse("q must be in the cache's dtype")
+    if out is None:
+        out = torch.empty(T, nH, cache.head_dim, dtype=cache.dtype, device=cache.device)
+    elif out.dtype is not cache.dtype or out.shape != q.shape:
+        _refuse("out must have q's shape and the cache's dtype")
+    os_ = _heads(out, "out", nH, cache.head_dim, dev)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or
+                            lse.get_device() != dev):
+        _refuse("lse must be a contiguous float32 tensor [T, heads]")
+    if ws is None:
+        ws = attend_paged_workspace(cache, T, nH, B)
+    with _on(dev, stream) as s:
+        _check(get_lib().dspark_attend_paged(
+            cache.ref, layer, q.data_ptr(), qs, nH, _vec(cu_new, "cu_new", torch.int32, B + 1, dev),
+            _vec(kv_len, "kv_len", torch.int32, B, dev), B, T, max_new, scale, 1 if causal else 0, window, out.data_ptr(),
+            os_, _ptr(lse), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), s))
+    return out
+
+
+def sample_workspace(rows: int, vocab: int, device="cuda"):
+    """A workspace for ``sample`` calls of up to this many rows and entries."""
+    import torch
+    return torch.empty(max(int(get_lib().dspark_sample_workspace_bytes(rows, vocab)), 256), dtype=torch.uint8, device=device)
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, ws=None, stream=None):
+    """One token per row of ``logits`` [rows, vocab] by temperature, top-k, top-p and min-p from the uniform
+    numbers ``u`` float32 [rows] (``dspark_sample``). The settings are tensors [rows] (``top_k`` int32, the
+    others float32) or None. Returns int32 tokens [rows]; ``probs`` float32 [rows] is filled if given."""
+    import torch
+    f32, dev = torch.float32, logits.get_device()
+    if logits.dim() != 2 or not logits.is_cuda or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        _refuse("logits must be a CUDA tensor [rows, vocab] with contiguous rows")
+    R, V = logits.shape
+    if tokens is None:
+        tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
+    if ws is None:
+        ws = sample_workspace(R, V, logits.device)
+    with _on(dev, stream) as s:
+        _check(get_lib().dspark_sample(
+            logits.data_ptr(), _dtype_code(logits.dtype), logits.stride(0), R, V, _vec(u, "u", f32, R, dev),
+            None if temperature is None else _vec(temperature, "temperature", f32, R, dev),
+            None if top_k is None else _vec(top_k, "top_k", torch.int32, R, dev),
+            None if top_p is None else _vec(top_p, "top_p", f32, R, dev),
+            None if min_p is None else _vec(min_p, "min_p", f32, R, dev), _vec(tokens, "tokens", torch.int32, R, dev),
+            None if probs is None else _vec(probs, "probs", f32, R, dev), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), s))
+    return tokens
 
 
 class KvCache:

@@ -1,0 +1,212 @@
+// dspark_norm_rope_paged: per-head RMS norms of q and k, the rotation at each
+// token's position, and the write of k and v into the pages, in one pass.
+//
+//   y = x / sqrt(mean(x^2) + eps) * gain          (v: no gain, or v as it is)
+//   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a),  a = position * inv_freq[i]
+// over the pairs (i, i + hd / 2). Bound by HBM: every element is read once and
+// written once. A thread owns eight consecutive elements of the head's first
+// half and the eight they turn with (two 16-byte loads of 16-bit rows), so the
+// rotation needs no exchange; the sum of squares is a shuffle over the head's
+// lanes. The angles are one table per token in shared memory, shared by its
+// heads: the turn count is reduced in 64 bits (at position 10^6 a 32-bit angle
+// is off by 0.03 rad), sine and cosine are taken of the fraction in 32 bits.
+#include "paged.h"
+
+namespace dspark {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct NormRopeParams {
+    const void* q; const void* k; const void* v; const void* q_norm; const void* k_norm;
+    int64_t q_stride, k_stride, v_stride;      // elements between tokens
+    const double* inv_freq; const int32_t* positions; const int64_t* slots;
+    void* q_out; void* kc; void* vc;
+    int32_t* status;
+    int64_t num_slots;
+    int T, nH, nKv, hd, lanes, v_norm, tokens;  // lanes: threads per head (a power of two); tokens: per block
+    float eps;
+};
+
+template <typename T> struct Raw8;             // eight elements as loaded
+template <> struct Raw8<float> { float4 a, b; };
+template <> struct Raw8<__half> { uint4 a; };
+template <> struct Raw8<__nv_bfloat16> { uint4 a; };
+
+__device__ __forceinline__ void load8(Raw8<float>& r, const float* p) {
+    r.a = *reinterpret_cast<const float4*>(p);
+    r.b = *reinterpret_cast<const float4*>(p + 4);
+}
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* p) { r.a = *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
+    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&x)[8]) {
+    const __half2* h = reinterpret_cast<const __half2*>(&r.a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { const float2 f = __half22float2(h[i]); x[2 * i] = f.x; x[2 * i + 1] = f.y; }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { const float2 f = __bfloat1622float2(h[i]); x[2 * i] = f.x; x[2 * i + 1] = f.y; }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
+    __half2 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+
+template <typename X, typename O>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams P) {
+    extern __shared__ float2 s_rot[];           // [tokens][hd / 2] (cos, sin)
+    const int tid = threadIdx.x, half = P.hd / 2;
+    const int t0 = blockIdx.x * P.tokens, nt = min(P.tokens, P.T - t0);
+    pdl_trigger();
+    pdl_wait();
+    for (int i = tid; i < nt * half; i += kThreads) {
+        const int t = i / half, j = i - t * half;
+        // turns = position * inv_freq / (2 pi), whole turns dropped in 64 bits
+        const double turns = (double)P.positions[t0 + t] * P.inv_freq[j] * 0.15915494309189533576888376337251;
+        float s, c;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        s_rot[i] = make_float2(c, s);
+    }
+    __syncthreads();
+    const int heads = P.nH + 2 * P.nKv, groups = kThreads / P.lanes;
+    const int grp = tid / P.lanes, l = tid % P.lanes, e = l * 8;
+    const bool mine = e < half;                 // hd = 192 and the like leave lanes idle
+    const int items = nt * heads;
+    for (int it0 = 0; it0 < items; it0 += groups) {
+        const int it = it0 + grp;
+        int t = 0, h = 0;
+        int64_t slot = -1;
+        if (it < items) {
+            t = it / heads;
+            h = it - t * heads;
+            slot = P.slots[t0 + t];
+            if (slot >= P.num_slots) {
+                set_status(P.status, DSPARK_DEV_CAPACITY);
+                slot = -1;
+            }
+        }
+        const bool on = slot >= 0 && mine;      // a negative slot is a padding row
+        const int kind = h < P.nH ? 0 : h < P.nH + P.nKv ? 1 : 2;
+        const int hh = kind == 0 ? h : kind == 1 ? h - P.nH : h - P.nH - P.nKv;
+        const X* src = kind == 0 ? static_cast<const X*>(P.q) + (t0 + t) * P.q_stride
+                     : kind == 1 ? static_cast<const X*>(P.k) + (t0 + t) * P.k_stride
+                                 : static_cast<const X*>(P.v) + (t0 + t) * P.v_stride;
+        src += (int64_t)hh * P.hd + e;
+        float x1[8], x2[8];
+        float ss = 0.f;
+        if (on) {
+            Raw8<X> r1, r2;
+            load8(r1, src);
+            load8(r2, src + half);
+            unpack8(r1, x1);
+            unpack8(r2, x2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += x1[i] * x1[i] + x2[i] * x2[i];
+        }
+        for (int o = P.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!on) continue;                      // lanes of a head agree except idle ones; the shuffle is behind
+        const float r = kind == 2 && !P.v_norm ? 1.f : 1.f / sqrtf(ss / (float)P.hd + P.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { x1[i] *= r; x2[i] *= r; }
+        if (kind < 2) {
+            const X* gain = static_cast<const X*>(kind == 0 ? P.q_norm : P.k_norm);
+            if (gain) {
+                Raw8<X> r1, r2;
+                float g1[8], g2[8];
+                load8(r1, gain + e);
+                load8(r2, gain + e + half);
+                unpack8(r1, g1);
+                unpack8(r2, g2);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { x1[i] *= g1[i]; x2[i] *= g2[i]; }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 cs = s_rot[t * half + e + i];
+                const float a = x1[i], b = x2[i];
+                x1[i] = a * cs.x - b * cs.y;
+                x2[i] = b * cs.x + a * cs.y;
+            }
+        }
+        O* dst = kind == 0 ? static_cast<O*>(P.q_out) + ((int64_t)(t0 + t) * P.nH + hh) * P.hd
+                           : static_cast<O*>(kind == 1 ? P.kc : P.vc) + (slot * P.nKv + hh) * P.hd;
+        store8(dst + e, x1);
+        store8(dst + e + half, x2);
+    }
+}
+
+template <typename X, typename O>
+cudaError_t launch(const NormRopeParams& P, cudaStream_t s) {
+    return launch_pdl(norm_rope_kernel<X, O>, dim3((P.T + P.tokens - 1) / P.tokens), dim3(kThreads),
+                      (size_t)P.tokens * (P.hd / 2) * sizeof(float2), s, P);
+}
+template <typename X>
+cudaError_t launch_x(const NormRopeParams& P, int dtype, cudaStream_t s) {
+    return dtype == DSPARK_DTYPE_F32 ? launch<X, float>(P, s)
+         : dtype == DSPARK_DTYPE_F16 ? launch<X, __half>(P, s) : launch<X, __nv_bfloat16>(P, s);
+}
+
+}  // namespace
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" int dspark_norm_rope_paged(const dspark_paged_cache* c, int32_t layer, int32_t x_dtype, const void* q,
+                                      int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                      int32_t n_heads, const void* q_norm, const void* k_norm, const double* inv_freq,
+                                      float eps, int32_t v_norm, const int32_t* positions, const int64_t* slots, int32_t T,
+                                      void* q_out, void* stream) {
+    const int rc = check_paged_cache(c);
+    if (rc != DSPARK_OK) return rc;
+    if (layer < 0 || layer >= c->layers) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "layer out of range");
+    if (!valid_dtype(x_dtype)) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "x_dtype must be fp32, bf16 or fp16");
+    if (n_heads < 1 || n_heads > (1 << 16)) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "n_heads must be in [1, 2^16]");
+    if (T < 0) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "T must be >= 0");
+    if (!(eps >= 0.f)) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+    if (T == 0) return DSPARK_OK;
+    if (!c->k || !c->v || !q || !k || !inv_freq || !positions || !slots || !q_out)
+        DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "cache.k, cache.v, q, k, inv_freq, positions, slots and q_out must be non-NULL");
+    if (!v) { v = k; v_stride = k_stride; }       // keys and values from one projection
+    const size_t es = dtype_bytes(x_dtype);
+    if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(q_out, 16) || !aligned_to(c->k, 16) ||
+        !aligned_to(c->v, 16) || !aligned_to(q_norm, 16) || !aligned_to(k_norm, 16))
+        DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "q, k, v, q_out, the gains and the cache must be 16-byte aligned");
+    if ((q_stride * (int64_t)es) % 16 || (k_stride * (int64_t)es) % 16 || (v_stride * (int64_t)es) % 16)
+        DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "the token strides of q, k and v must be multiples of 16 bytes");
+    NormRopeParams P{};
+    P.q = q; P.k = k; P.v = v; P.q_norm = q_norm; P.k_norm = k_norm;
+    P.q_stride = q_stride; P.k_stride = k_stride; P.v_stride = v_stride;
+    P.inv_freq = inv_freq; P.positions = positions; P.slots = slots; P.q_out = q_out;
+    const size_t layer_bytes = (size_t)paged_layer_elems(*c) * dtype_bytes(c->dtype) * layer;
+    P.kc = static_cast<char*>(c->k) + layer_bytes;
+    P.vc = static_cast<char*>(c->v) + layer_bytes;
+    P.status = c->status; P.num_slots = (int64_t)c->num_pages * c->page_size;
+    P.T = T; P.nH = n_heads; P.nKv = c->n_kv; P.hd = c->head_dim; P.v_norm = v_norm != 0; P.eps = eps;
+    P.lanes = 1;
+    while (P.lanes * 16 < P.hd) P.lanes *= 2;
+    P.tokens = 1;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = x_dtype == DSPARK_DTYPE_F32 ? launch_x<float>(P, c->dtype, s)
+                  : x_dtype == DSPARK_DTYPE_F16 ? launch_x<__half>(P, c->dtype, s)
+                                                : launch_x<__nv_bfloat16>(P, c->dtype, s);
+    if (e != cudaSuccess) DSPARK_FAIL(DSPARK_ERR_CUDA, std::string("norm rope launch: ") + cudaGetErrorString(e));
+    return DSPARK_OK;
+}

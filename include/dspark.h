@@ -50,6 +50,7 @@ extern "C" {
 #define DSPARK_DEV_WAIT_TIMEOUT  4  /* a bounded device wait gave up */
 #define DSPARK_DEV_CAPACITY      8  /* an append was refused on the device (a count outside [0, Lnew_max] or past capacity) */
 #define DSPARK_DEV_RANGE        16  /* a 4-bit model's context row held a value outside fp16's range (|x| > 65504) */
+#define DSPARK_DEV_BAD_PAGE     32  /* a block table or free list named a page outside [0, num_pages) */
 
 #define DSPARK_DTYPE_F32  0
 #define DSPARK_DTYPE_BF16 1
@@ -368,6 +369,153 @@ int dspark_attend(const dspark_model* model, int32_t layer, const dspark_kv_cach
 int dspark_attend_no_alloc(const dspark_model* model, int32_t layer, const dspark_kv_cache* cache,
                            const void* q, const void* k_blk, const void* v_blk, void* out,
                            int32_t A, int32_t max_ctx_len, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The target's verification step over a paged K/V cache (no counterpart on the
+ * pages, which leave the target model's cache to its host). After a draft
+ * round the target checks the block: dspark_page_slots gives the new tokens
+ * their pages, dspark_norm_rope_paged finishes the heads of the target's
+ * products and writes k and v into those pages, dspark_attend_paged attends
+ * over them, and dspark_sample draws tokens from the target's logits. The
+ * target's matrix products are the caller's. These calls take no model; they
+ * run on the current device, which must be the one that holds their buffers.
+ *
+ * k, v: device KV [layers][num_pages][page_size][n_kv][head_dim]; the layers
+ * share the block table. Key j of batch row b is row j % page_size of page
+ * block_table[b][j / page_size].
+ *   block_table  device int32 [batch][max_pages]
+ *   status       device int32 word that the kernels OR DSPARK_DEV_* bits
+ *                into, or NULL; the caller clears and reads it
+ *   head_dim     a multiple of 16 in [16, 256]
+ *   dtype        DSPARK_DTYPE_* of the K/V, of the queries and of the attention's output
+ * ---------------------------------------------------------------------------
+ */
+typedef struct dspark_paged_cache {
+    void*    k;
+    void*    v;
+    int32_t* block_table;
+    int32_t* status;
+    int32_t  layers;
+    int32_t  num_pages;
+    int32_t  page_size;
+    int32_t  n_kv;
+    int32_t  head_dim;
+    int32_t  batch;
+    int32_t  max_pages;
+    int32_t  dtype;
+} dspark_paged_cache;
+
+/*
+ * Pages, block tables and slots of a step's new tokens, from lengths that live
+ * on the device. Request b < B has ctx_len[b] cached rows, n_new[b] new tokens
+ * and holds n_pages[b] pages (block_table[b][0 .. n_pages[b])). It needs
+ * ceil((ctx_len[b] + n_new[b]) / page_size); the missing ones come off the top
+ * of the free stack in request order (the page taken r-th is
+ * free_pages[free_count - 1 - r]) and are written into its block table row.
+ *   ctx_len, n_new, n_pages  device int32 [B]
+ *   free_pages  device int32 [n_free], of which the first free_count[0] are free
+ *   max_tokens  host: entries of slots and positions
+ *   n_pages_out   device int32 [B]; free_count_out device int32 [1]
+ *   cu_new        device int32 [B + 1]: exclusive sums of n_new
+ *   kv_len        device int32 [B]: ctx_len + n_new
+ *   slots         device int64 [max_tokens]: page * page_size + row of token t
+ *                 (request b's tokens are [cu_new[b], cu_new[b + 1])), -1 past the last
+ *   positions     device int32 [max_tokens]: ctx_len[b] + t - cu_new[b], 0 past the last
+ * An output may be its input's own array (n_pages_out = n_pages, free_count_out =
+ * free_count, kv_len = ctx_len). The lengths are checked on the device before
+ * anything is taken: a negative number, a request past max_pages, more new tokens
+ * than max_tokens or more pages than are free refuse the whole call, with
+ * DSPARK_DEV_CAPACITY in the cache's status: cu_new is then 0 throughout, every
+ * slot -1, kv_len = ctx_len, and pages, counts and tables stay as they were. A page number outside
+ * [0, num_pages) sets DSPARK_DEV_BAD_PAGE and gives its tokens slot -1. cache.k
+ * and cache.v are not read. B <= 4096.
+ */
+int dspark_page_slots(const dspark_paged_cache* cache, const int32_t* ctx_len, const int32_t* n_new, int32_t B,
+                      const int32_t* n_pages, const int32_t* free_pages, int32_t n_free, const int32_t* free_count,
+                      int32_t max_tokens, int32_t* n_pages_out, int32_t* free_count_out, int32_t* cu_new,
+                      int32_t* kv_len, int64_t* slots, int32_t* positions, void* stream);
+
+/*
+ * Per-head RMS norms of q and k, the rotation, and the write of k and v into the
+ * pages, in one pass. For token t < T with slots[t] >= 0:
+ *   q_out[t,h] = rope(q[t,h] / sqrt(mean(q[t,h]^2) + eps) * q_norm, positions[t])
+ *   k row of slot slots[t] = rope(k[t,g] / sqrt(mean(k[t,g]^2) + eps) * k_norm, positions[t])
+ *   v row of slot slots[t] = v[t,g] / sqrt(mean(v[t,g]^2) + eps) with v_norm, else v[t,g]
+ * The rotation turns lane i with lane i + head_dim / 2 by positions[t] *
+ * inv_freq[i] (rotate-half, as the draft's own heads; 0 = identity lane); the
+ * angle is formed in 64 bits. A token whose slot is negative is padding: nothing
+ * is read or written for it. A slot past num_pages * page_size is skipped
+ * likewise and sets DSPARK_DEV_CAPACITY. Two tokens of one call must not share
+ * a slot (either's row may remain).
+ *   q  device X [T][n_heads][head_dim], k, v device X [T][n_kv][head_dim], X = x_dtype, with
+ *      q_stride, k_stride, v_stride elements between tokens (multiples of 16 bytes; the
+ *      three may be slices of one product); v NULL: the values come from k's product
+ *   q_norm, k_norm  device X [head_dim], or NULL: gain 1
+ *   inv_freq   device double [head_dim / 2]
+ *   positions  device int32 [T]; slots device int64 [T]
+ *   q_out      device KV [T][n_heads][head_dim]
+ * Arithmetic in fp32, rounded once to the cache's type. Pointers are 16-byte aligned.
+ */
+int dspark_norm_rope_paged(const dspark_paged_cache* cache, int32_t layer, int32_t x_dtype, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           int32_t n_heads, const void* q_norm, const void* k_norm, const double* inv_freq, float eps,
+                           int32_t v_norm, const int32_t* positions, const int64_t* slots, int32_t T, void* q_out,
+                           void* stream);
+
+/*
+ * Attention of each request's new tokens over its pages. Request b < B has the
+ * queries [cu_new[b], cu_new[b + 1]), which are the last of its kv_len[b] keys:
+ * its i-th sits at key kv_len[b] - n + i, n = cu_new[b + 1] - cu_new[b]. It sees the keys
+ * j < kv_len[b], with causal j <= its own, with window > 0 also j > its own -
+ * window. Query head h reads kv head h / (n_heads / n_kv):
+ *   out[t,h] = sum_j softmax_j(scale q[t,h] . K[j,g]) V[j,g],  lse[t,h] = log sum_j exp(scale q . K[j])
+ * A query that sees no key gets zeros and lse = -infinity; rows of no request
+ * (at or past cu_new[B]) stay as they were.
+ *   q    device KV [T][n_heads][head_dim], q_stride elements between tokens
+ *   cu_new  device int32 [B + 1], ascending, at most T; kv_len device int32 [B]
+ *   max_new host: an upper bound of n over the requests (chooses the kernel's tiles)
+ *   scale   positive, finite
+ *   out  device KV [T][n_heads][head_dim], out_stride elements between tokens (not q's memory)
+ *   lse  device float [T][n_heads] or NULL
+ *   ws   >= dspark_attend_paged_workspace_bytes(cache, T, n_heads, B), 256-byte aligned; calls
+ *        that may overlap on the GPU need one each
+ * Scores, softmax and sums are fp32; the probabilities that multiply V are rounded to KV.
+ * Cache rows that no query of a request sees are never used, whatever they hold; a row that some query
+ * sees must be finite. Lengths past max_pages * page_size are clamped (DSPARK_DEV_BAD_LENGTH); a page
+ * outside [0, num_pages) reads as zeros (DSPARK_DEV_BAD_PAGE). A kernel whose copies never arrive
+ * gives up (DSPARK_DEV_WAIT_TIMEOUT). bf16 and fp16 caches with head_dim a multiple of 64
+ * and page_size a power of two >= 8 run on the tensor cores, others on the CUDA cores. q, out, k
+ * and v are 16-byte aligned, the strides multiples of 16 bytes.
+ */
+size_t dspark_attend_paged_workspace_bytes(const dspark_paged_cache* cache, int32_t T, int32_t n_heads, int32_t B);
+int dspark_attend_paged(const dspark_paged_cache* cache, int32_t layer, const void* q, int64_t q_stride,
+                        int32_t n_heads, const int32_t* cu_new, const int32_t* kv_len, int32_t B, int32_t T,
+                        int32_t max_new, float scale, int32_t causal, int32_t window, void* out, int64_t out_stride,
+                        float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One token per row of logits from a given uniform number. Row r with
+ * temperature T <= 0: the largest logit (lowest index on ties). Else, with weights
+ * w_i = exp((x_i - max x) / T) and the candidates in falling order (equal logits: the lower
+ * index first): top_k > 0 keeps the first top_k; top_p < 1, of those, the shortest prefix
+ * whose weight reaches top_p of theirs (at least one); min_p > 0 those with w_i >=
+ * min_p. The token is the first i, in the vocabulary's order, whose cumulative kept
+ * weight exceeds u times the kept total (the last kept one where u >= 1).
+ *   logits  device T [rows][vocab], T = dtype, row_stride elements between rows; a NaN counts as -infinity
+ *   u       device float [rows], in [0, 1)
+ *   temperature, top_p, min_p  device float [rows]; top_k device int32 [rows]; each may be
+ *           NULL (1, 1, 0 and 0: not filtered)
+ *   tokens  device int32 [rows]; -1 for a row without a logit above -infinity
+ *   probs   device float [rows] or NULL: the token's share of the kept weight
+ *   ws      >= dspark_sample_workspace_bytes(rows, vocab), 256-byte aligned; calls that may
+ *           overlap on the GPU need one each
+ * Weights and their sums are formed in 64 bits; a weight below 2^-62 of their sum counts as 0. vocab <= 2^24.
+ */
+size_t dspark_sample_workspace_bytes(int32_t rows, int32_t vocab);
+int dspark_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t rows, int32_t vocab, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                  int32_t* tokens, float* probs, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Test-facing dump of every layer's attention output (the parity check of the

@@ -1,0 +1,131 @@
+"""sample against float64: tokens equal, shares within the roundings of one division and one fp32 result."""
+import numpy as np
+import pytest
+import torch
+
+from paged_util import DT, ref_sample
+from parity_util import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    ensure_built()
+
+
+def check(x, u, **kw):
+    """x: torch logits on the CPU; kw: numpy settings."""
+    import block_draft_model_dspark_b200 as dsp
+    R, V = x.shape
+    dev = {k: torch.from_numpy(v).cuda() for k, v in kw.items()}
+    probs = torch.full((R,), -5.0, device="cuda")
+    tok = dsp.sample(x.cuda(), torch.from_numpy(u).cuda(), probs=probs, **dev)
+    want, prob, margin = ref_sample(x.float().numpy(), u, **kw)
+    # 64-bit sums of V terms: u * total is known to V 2^-52 of the total on either side
+    sure = margin > V * 2.0 ** -50
+    assert sure[u > 0].mean() > 0.9                 # u = 0 is itself an edge where weights vanish
+    got = tok.cpu().numpy()
+    assert np.array_equal(got[sure], want[sure]), (np.nonzero(got != want)[0][:5], got[got != want][:5], want[got != want][:5])
+    np.testing.assert_allclose(probs.cpu().numpy()[sure], prob[sure], rtol=2.0 ** -23, atol=2.0 ** -149)
+
+
+def logits(seed, R, V, dt, spread=2.5, peaks=8):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((R, V)) * spread
+    for r in range(R):
+        x[r, rng.integers(0, V, peaks)] += 6 + 3 * rng.random(peaks)
+    return torch.from_numpy(x.astype(np.float32)).to(DT[dt]), rng
+
+
+def settings(rng, R):
+    pick = lambda t, off, share: np.where(rng.random(R) < share, t, off)  # noqa: E731
+    return dict(temperature=pick(0.3 + rng.random(R) * 1.2, 0.0, 0.9).astype(np.float32), top_k=pick(rng.integers(1, 80, R), 0, 0.5).astype(np.int32),
+                top_p=pick(0.3 + 0.7 * rng.random(R), 1.0, 0.6).astype(np.float32), min_p=pick(0.2 * rng.random(R), 0.0, 0.4).astype(np.float32))
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("R,V", [(1, 1), (5, 2), (40, 33), (64, 1000), (33, 32003), (20, 50257), (6, 262144)])
+def test_sample_matches_reference(dt, R, V):
+    x, rng = logits(R * 7 + V, R, V, dt)
+    check(x, rng.random(R, dtype=np.float32), **settings(rng, R))
+    check(x, rng.random(R, dtype=np.float32))
+
+
+@pytest.mark.parametrize("name", ["temperature", "top_k", "top_p", "min_p"])
+def test_each_filter_alone(name):
+    x, rng = logits(1, 200, 3001, "fp32", spread=1.5)
+    check(x, rng.random(200, dtype=np.float32), **{name: settings(rng, 200)[name]})
+
+
+def test_flat_rows_keep_many_candidates():
+    """Prefixes of tens of thousands: top-p of a flat row, and a top-k above every short list."""
+    x, rng = logits(2, 12, 100003, "fp32", spread=0.5, peaks=1)
+    u = rng.random(12, dtype=np.float32)
+    check(x, u, top_p=np.full(12, 0.95, np.float32))
+    check(x, u, top_k=np.full(12, 60000, np.int32))
+    check(x, u, top_k=np.full(12, 60000, np.int32), top_p=np.full(12, 0.9, np.float32), temperature=np.full(12, 0.8, np.float32))
+    check(x, u, top_k=np.full(12, 100003, np.int32), min_p=np.full(12, 0.5, np.float32))
+
+
+@pytest.mark.parametrize("V", [7, 5000, 70001])
+def test_ties_go_to_the_lower_index(V):
+    """Few distinct values: every boundary falls among equal logits."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.integers(0, 4, (30, V)).astype(np.float32))
+    x[0] = 1.0
+    x[1] = torch.where(torch.arange(V) % 2 == 0, 0.0, -0.0)
+    u = rng.random(30, dtype=np.float32)
+    check(x, u, temperature=np.full(30, 0.0, np.float32))
+    k = rng.integers(1, V + 1, 30).astype(np.int32)
+    check(x, u, top_k=k)
+    # masses of small integers' weights: an exact edge may fall either way, so p is irrational enough
+    check(x, u, top_p=(0.2 + 0.7 * rng.random(30)).astype(np.float32), top_k=k)
+    check(x, u, min_p=np.full(30, 0.3, np.float32))
+
+
+def test_masked_and_special_logits():
+    V = 4099
+    x, rng = logits(4, 12, V, "fp32")
+    inf = float("inf")
+    x[0] = -inf                                     # nothing to choose from
+    x[1] = -inf
+    x[1, 77] = -3.0                                 # one choice
+    x[2, ::2] = -inf
+    x[3, 5] = float("nan")
+    x[4] = float("nan")
+    x[5, 9] = inf
+    x[6, [9, 4000]] = inf
+    x[7] = torch.finfo(torch.float32).min           # a mask's lowest value everywhere: flat
+    x[8, 100:] = torch.finfo(torch.float32).min
+    x[9] *= 1e30
+    u = rng.random(12, dtype=np.float32)
+    check(x, u)
+    check(x, u, temperature=np.zeros(12, np.float32))
+    check(x, u, top_k=np.full(12, 3, np.int32), top_p=np.full(12, 0.7, np.float32))
+    check(x, u, top_p=np.full(12, 0.7, np.float32), min_p=np.full(12, 0.01, np.float32))
+
+
+def test_extreme_settings():
+    x, rng = logits(5, 16, 2000, "fp32")
+    u = rng.random(16, dtype=np.float32)
+    u[:4] = [0.0, np.float32(1) - np.float32(2) ** -24, 0.0, 0.5]
+    check(x, u, top_p=np.zeros(16, np.float32))
+    check(x, u, min_p=np.ones(16, np.float32))
+    check(x, u, top_k=np.ones(16, np.int32))
+    check(x, u, temperature=np.full(16, 1e-30, np.float32))
+    check(x, u, temperature=np.full(16, 1e30, np.float32))
+    check(x, u, top_k=np.full(16, -1, np.int32), top_p=np.full(16, 2.0, np.float32), min_p=np.full(16, -1.0, np.float32))
+
+
+def test_strided_rows_and_unaligned_starts():
+    import block_draft_model_dspark_b200 as dsp
+    x, rng = logits(6, 9, 1003, "bf16")
+    u = rng.random(9, dtype=np.float32)
+    wide = torch.full((9, 1500), 50.0, dtype=torch.bfloat16)
+    wide[:, 101:1104] = x
+    got = dsp.sample(wide.cuda()[:, 101:1104], torch.from_numpy(u).cuda())
+    assert np.array_equal(got.cpu().numpy(), ref_sample(x.float().numpy(), u)[0])
+    assert dsp.sample(x.cuda()[:0], torch.zeros(0, device="cuda")).shape == (0,)

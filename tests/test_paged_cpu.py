@@ -1,0 +1,122 @@
+"""The paged verification step's C entry points without a GPU: every refusal returns its code, with a message,
+before anything is launched (the pointers here are numbers that nothing may touch)."""
+import ctypes
+
+import pytest
+
+P = 4096            # an aligned address that is never read
+
+
+@pytest.fixture(scope="module")
+def dsp():
+    from block_draft_model_dspark_b200 import build
+    build.build()
+    import block_draft_model_dspark_b200 as d
+    d.get_lib()
+    return d
+
+
+def cache(dsp, **kw):
+    c = dsp.dspark_paged_cache()
+    c.k = c.v = c.block_table = P
+    c.layers, c.num_pages, c.page_size, c.n_kv, c.head_dim, c.batch, c.max_pages, c.dtype = 2, 10, 16, 2, 128, 8, 4, dsp.DSPARK_DTYPE_F16
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def refused(dsp, rc, code):
+    assert rc == code and dsp.get_lib().dspark_last_error().decode()
+
+
+BAD_CACHES = [(dict(layers=0), -1), (dict(num_pages=0), -1), (dict(page_size=0), -1), (dict(n_kv=0), -1), (dict(batch=0), -1), (dict(max_pages=0), -1),
+              (dict(dtype=3), -1), (dict(head_dim=0), -2), (dict(head_dim=100), -2), (dict(head_dim=512), -2), (dict(block_table=None), -1),
+              (dict(page_size=1 << 21), -2), (dict(n_kv=1 << 17), -2)]
+
+
+def slots_args(c, **kw):
+    a = dict(cache=ctypes.addressof(c), ctx_len=P, n_new=P, B=8, n_pages=P, free_pages=P, n_free=4, free_count=P, max_tokens=5, n_pages_out=P,
+             free_count_out=P, cu_new=P, kv_len=P, slots=P, positions=P, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def norm_args(c, **kw):
+    a = dict(cache=ctypes.addressof(c), layer=1, x_dtype=1, q=P, q_stride=1024, k=P, k_stride=1024, v=P, v_stride=1024, n_heads=4, q_norm=P, k_norm=P,
+             inv_freq=P, eps=1e-6, v_norm=0, positions=P, slots=P, T=3, q_out=P, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def attend_args(c, **kw):
+    a = dict(cache=ctypes.addressof(c), layer=1, q=P, q_stride=512, n_heads=4, cu_new=P, kv_len=P, B=8, T=3, max_new=2, scale=0.1, causal=1, window=0,
+             out=P, out_stride=512, lse=None, ws=P, ws_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def sample_args(**kw):
+    a = dict(logits=P, dtype=0, row_stride=100, rows=2, vocab=100, u=P, temperature=None, top_k=None, top_p=None, min_p=None, tokens=P, probs=None, ws=P,
+             ws_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_bad_caches(dsp, kw, code):
+    lib, c = dsp.get_lib(), cache(dsp, **kw)
+    refused(dsp, lib.dspark_page_slots(*slots_args(c)), code)
+    refused(dsp, lib.dspark_norm_rope_paged(*norm_args(c)), code)
+    refused(dsp, lib.dspark_attend_paged(*attend_args(c)), code)
+    assert lib.dspark_attend_paged_workspace_bytes(ctypes.addressof(c), 10, 4, 8) == 0
+
+
+def test_page_slots_refusals(dsp):
+    lib, c = dsp.get_lib(), cache(dsp)
+    refused(dsp, lib.dspark_page_slots(*slots_args(c, cache=None)), -1)
+    for kw in (dict(B=0), dict(B=9), dict(max_tokens=-1), dict(n_free=-1)) + tuple({n: None} for n in
+               ("ctx_len", "n_new", "n_pages", "free_pages", "free_count", "n_pages_out", "free_count_out", "cu_new", "kv_len", "slots", "positions")):
+        refused(dsp, lib.dspark_page_slots(*slots_args(c, **kw)), -1)
+    big = cache(dsp, batch=5000)
+    refused(dsp, lib.dspark_page_slots(*slots_args(big, B=4097)), -2)
+
+
+def test_norm_rope_refusals(dsp):
+    lib, c = dsp.get_lib(), cache(dsp)
+    for kw in (dict(layer=-1), dict(layer=2), dict(x_dtype=7), dict(n_heads=0), dict(T=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(q=P + 8), dict(k=P + 2),
+               dict(v=P + 8), dict(q_out=P + 8), dict(q_norm=P + 8), dict(k_norm=P + 4), dict(q_stride=1001), dict(k_stride=4), dict(v_stride=2)) + \
+            tuple({n: None} for n in ("q", "k", "inv_freq", "positions", "slots", "q_out")):
+        refused(dsp, lib.dspark_norm_rope_paged(*norm_args(c, **kw)), -1)
+    for kw in (dict(k=None), dict(v=None), dict(k=P + 8)):
+        bad = cache(dsp, **kw)
+        refused(dsp, lib.dspark_norm_rope_paged(*norm_args(bad)), -1)
+    assert lib.dspark_norm_rope_paged(*norm_args(c, T=0, q=None, k=None)) == 0
+
+
+def test_attend_refusals(dsp):
+    lib, c = dsp.get_lib(), cache(dsp)
+    for kw in (dict(layer=-1), dict(layer=2), dict(n_heads=0), dict(n_heads=3), dict(B=-1), dict(B=9), dict(T=-1), dict(max_new=-1), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(q=P + 8), dict(out=P + 8), dict(ws=P + 16),
+               dict(q_stride=100), dict(out_stride=100), dict(q_stride=-512), dict(out_stride=-512)) + tuple({n: None} for n in ("q", "out", "cu_new", "kv_len", "ws")):
+        refused(dsp, lib.dspark_attend_paged(*attend_args(c, **kw)), -1)
+    for kw in (dict(k=None), dict(v=None), dict(k=P + 8), dict(v=P + 8)):
+        bad = cache(dsp, **kw)
+        refused(dsp, lib.dspark_attend_paged(*attend_args(bad)), -1)
+    need = lib.dspark_attend_paged_workspace_bytes(ctypes.addressof(c), 3, 4, 8)
+    assert need > 0
+    refused(dsp, lib.dspark_attend_paged(*attend_args(c, ws_bytes=need - 1)), -4)
+    refused(dsp, lib.dspark_attend_paged(*attend_args(c, T=1 << 30)), -2)
+    assert lib.dspark_attend_paged(*attend_args(c, T=0, q=None)) == 0
+    assert lib.dspark_attend_paged(*attend_args(c, B=0, kv_len=None)) == 0
+
+
+def test_sample_refusals(dsp):
+    lib = dsp.get_lib()
+    for kw in (dict(dtype=5), dict(rows=-1), dict(vocab=0), dict(row_stride=99), dict(logits=None), dict(u=None), dict(tokens=None), dict(ws=None),
+               dict(logits=P + 2), dict(ws=P + 16)):
+        refused(dsp, lib.dspark_sample(*sample_args(**kw)), -1)
+    refused(dsp, lib.dspark_sample(*sample_args(vocab=(1 << 24) + 1, row_stride=1 << 25)), -2)
+    need = lib.dspark_sample_workspace_bytes(2, 100)
+    assert need > 0 and lib.dspark_sample_workspace_bytes(-1, 100) == 0 and lib.dspark_sample_workspace_bytes(1, 0) == 0
+    refused(dsp, lib.dspark_sample(*sample_args(ws_bytes=need - 1)), -4)
+    assert lib.dspark_sample(*sample_args(rows=0, logits=None)) == 0
