@@ -7,6 +7,8 @@
 // over the keys j that query t sees. One warp per (token, query head): 32 keys
 // at a time, a lane per key for the scores, then a lane per head dimension for
 // the values; one pass with the running maximum and sum in 32 bits.
+#include <algorithm>
+
 #include "paged.h"
 
 namespace dspark {
@@ -33,9 +35,10 @@ __global__ void __launch_bounds__(kWarps * 32) attend_paged_simt_kernel(PagedAtt
     const int c0 = P.cu[b], c1 = P.cu[b + 1];
     if (t < c0 || t >= c1) return;                     // a row of no request stays as it was
     int L = P.kv_len[b];
-    if (L < 0 || (int64_t)L > (int64_t)P.max_pages * P.page_size) {
+    const int cap = (int)min((int64_t)kMaxKeys, (int64_t)P.max_pages * P.page_size);
+    if (L < 0 || L > cap) {
         if (lane == 0) set_status(P.status, DSPARK_DEV_BAD_LENGTH);
-        L = (int)min((int64_t)max(L, 0), (int64_t)P.max_pages * P.page_size);
+        L = min(max(L, 0), cap);
     }
     const int pos = L - (c1 - c0) + (t - c0);          // the query's own key
     const int end = P.causal ? min(L, pos + 1) : L;
@@ -109,7 +112,7 @@ using namespace dspark;
 
 extern "C" size_t dspark_attend_paged_workspace_bytes(const dspark_paged_cache* c, int32_t T, int32_t n_heads, int32_t B) {
     if (check_paged_cache(c) != DSPARK_OK || T < 0 || n_heads < 1 || B < 0) return 0;
-    return 256;
+    return tc::attend_paged_tc_supported(*c, n_heads) ? tc::attend_paged_tc_workspace(c->head_dim) : 256;
 }
 
 extern "C" int dspark_attend_paged(const dspark_paged_cache* c, int32_t layer, const void* q, int64_t q_stride,
@@ -122,6 +125,7 @@ extern "C" int dspark_attend_paged(const dspark_paged_cache* c, int32_t layer, c
     if (n_heads < 1 || n_heads % c->n_kv != 0)
         DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "n_heads must be a positive multiple of the cache's n_kv");
     if (B < 0 || B > c->batch) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "B must be in [0, cache.batch]");
+    if (B > tc::attend_paged_max_batch()) DSPARK_FAIL(DSPARK_ERR_UNSUPPORTED, "more than 4096 requests in one call");
     if (T < 0 || max_new < 0) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "T and max_new must be >= 0");
     if (!(scale > 0.f) || scale > 3.0e38f) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "scale must be positive and finite");
     if (window < 0) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "window must be >= 0 (0: none)");
@@ -133,19 +137,25 @@ extern "C" int dspark_attend_paged(const dspark_paged_cache* c, int32_t layer, c
         DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "q, out and the cache must be 16-byte aligned, ws 256-byte aligned");
     if ((q_stride * (int64_t)es) % 16 || (out_stride * (int64_t)es) % 16 || q_stride < 0 || out_stride < 0)
         DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "the token strides of q and out must be non-negative multiples of 16 bytes");
+    const int64_t row = (int64_t)n_heads * c->head_dim;
+    if (T > 1 && (q_stride < row || out_stride < row))
+        DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "the token strides of q and out must be at least n_heads * head_dim");
+    if (q_stride >= ((int64_t)1 << 38)) DSPARK_FAIL(DSPARK_ERR_UNSUPPORTED, "q_stride at or above 2^38");
     if ((int64_t)T * n_heads > ((int64_t)1 << 31) - 1) DSPARK_FAIL(DSPARK_ERR_UNSUPPORTED, "T * n_heads above 2^31 - 1");
     if (ws_bytes < dspark_attend_paged_workspace_bytes(c, T, n_heads, B))
         DSPARK_FAIL(DSPARK_ERR_WORKSPACE, "ws smaller than dspark_attend_paged_workspace_bytes()");
     PagedAttn a{};
-    a.q = q; a.out = out; a.lse = lse; a.q_stride = q_stride; a.out_stride = out_stride;
+    a.q = q; a.out = out; a.lse = lse; a.q_stride = T > 1 ? q_stride : row; a.out_stride = T > 1 ? out_stride : row;
     const size_t layer_bytes = (size_t)paged_layer_elems(*c) * es * layer;
     a.k = static_cast<const char*>(c->k) + layer_bytes;
     a.v = static_cast<const char*>(c->v) + layer_bytes;
     a.table = c->block_table; a.cu = cu_new; a.kv_len = kv_len; a.status = c->status;
     a.T = T; a.B = B; a.nH = n_heads; a.nKv = c->n_kv; a.grp = n_heads / c->n_kv; a.hd = c->head_dim;
     a.max_pages = c->max_pages; a.num_pages = c->num_pages; a.page_size = c->page_size; a.dtype = c->dtype;
-    a.max_new = max_new; a.scale = scale; a.causal = causal != 0; a.window = window;
-    cudaError_t e = launch_attend_paged_simt(a, static_cast<cudaStream_t>(stream));
+    a.max_new = max_new; a.scale = scale; a.causal = causal != 0;
+    a.window = window >= std::min((int64_t)kMaxKeys, (int64_t)c->max_pages * c->page_size) ? 0 : window;   // wider than any request: none
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = tc::attend_paged_tc_supported(*c, n_heads) ? tc::launch_attend_paged_tc(a, ws, s) : launch_attend_paged_simt(a, s);
     if (e != cudaSuccess) DSPARK_FAIL(DSPARK_ERR_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
     return DSPARK_OK;
 }

@@ -1,0 +1,827 @@
+// dspark_attend_paged on the tcgen05 tensor cores (bf16 or fp16 caches, head_dim
+// a multiple of 64, pages of a power of two >= 8 rows).
+//
+// A unit is up to NQ query tiles of one (request, kv head): the grp query heads
+// that share the kv head times tpt = 128 / grp tokens fill the 128 rows of a tile
+// (row r = token r / grp, head r % grp), so K and V are read once for all of them. Its
+// key tiles of KT rows are gathered from the pages by TMA, one request per page
+// and 64 dimensions, into the swizzled layout the MMAs read.
+//   S = Q K^T -> TMEM (two buffers); P = exp2(scale log2(e) (S - m)) -> TMEM over
+//   its S buffer, in the cache's type (both operands of an MMA have one type;
+//   the sums take the unrounded P); O += P V -> TMEM.
+// The running maximum m is raised only when a tile's exceeds it by 8 (log2), so O
+// is rarely rescaled; P stays below 256.
+//
+// Steps: with NQ = 2 (prompt chunks, head_dim <= 128, KT = 128) step s is tile s / 2 of
+// query tile s % 2, with NQ = 1 it is tile s; step s uses S buffer s % 2. The
+// MMA thread issues S(0), S(1), then PV(s), S(s + 2): while one buffer is in the softmax
+// the tensor cores work on the other. MMAs of one thread run in order, so S(s + 2) may
+// overwrite the P that PV(s) reads. head_dim 192 and 256 keep Q in tensor memory (O, two
+// S buffers of 64 columns and Q fill its 512 columns): with Q in shared
+// memory the S product would read 192 bytes a cycle, above the 128 it can.
+//
+// Work split: the units' tiles (plus kUnitCost a unit for its fixed work), laid end to
+// end, are cut into equal contiguous shares, one per CTA, whatever the
+// requests' lengths (which only the device knows): a plan kernel finds each share's
+// start and the units that a cut crosses. Those units' pieces write O / l (fp32) and (m, l)
+// per row, which a merge kernel joins in order: results do not depend on timing.
+//
+// Warp roles: NQ * 4 softmax warps (thread = query row = TMEM lane), then one warp
+// each for the loads, the MMAs, and zeroing V rows outside the unit's keys (those
+// rows may hold anything; P = 0 times NaN would poison O. K needs no care:
+// masked scores are replaced). Every wait is bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged.h"
+#include "tc_ptx.cuh"
+
+namespace dspark {
+namespace tc {
+namespace {
+
+constexpr int kGrid = 148;           // shares: one CTA per SM of a B200
+constexpr int kUnitCost = 2;         // a unit's fixed work (query tile, first load, epilogue) in tiles
+constexpr int kRows = 128;           // rows of a query tile: the MMAs' M
+constexpr int kMaxBatch = 4096;
+constexpr float kRescale = 8.0f;     // log2 headroom before the running maximum is raised
+constexpr int kPlanThreads = 512;
+constexpr size_t kSmemMax = 232448;
+
+struct Share { int b, g, qt, x; int64_t len; };          // first unit, offset in it, total length (cost units)
+struct MergeUnit { int b, g, qt, c0, odd, c1; };         // pieces: slot 2 c0 + odd, then slots 2 (c0 + 1) .. 2 c1; c1 < 0: none
+
+struct Params {
+    PagedAttn a;
+    Share* shares; MergeUnit* merges;
+    float* part_o; float* part_ml;   // [2 kGrid][NQ * 128][hd], [..][2]
+    int tpt, tpu;                    // tokens per query tile, per unit
+    int page_shift;
+    int32_t* status;
+};
+
+// Request b as every role sees it.
+struct Req { int t0, n, L; };
+__device__ __forceinline__ Req load_req(const PagedAttn& a, int b) {
+    Req r;
+    r.t0 = min(max(a.cu[b], 0), a.T);
+    r.n = min(max(a.cu[b + 1], r.t0), a.T) - r.t0;
+    r.L = (int)min((int64_t)min(max(a.kv_len[b], 0), kMaxKeys), (int64_t)a.max_pages * a.page_size);
+    return r;
+}
+// The keys [lo, hi) that some query of unit qt sees (hi <= lo: none).
+template <int KT>
+__device__ __forceinline__ void unit_keys(const PagedAttn& a, const Req& r, int tpu, int qt, int* lo, int* hi) {
+    const int i0 = qt * tpu, i1 = min(r.n, i0 + tpu) - 1;     // its tokens
+    const int p0 = r.L - r.n + i0, p1 = r.L - r.n + i1;       // their keys
+    *hi = a.causal ? min(r.L, p1 + 1) : r.L;
+    *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    if (*hi <= *lo) *hi = *lo = 0;
+}
+template <int KT>
+__device__ __forceinline__ int unit_tiles(const PagedAttn& a, const Req& r, int tpu, int qt) {
+    int lo, hi;
+    unit_keys<KT>(a, r, tpu, qt, &lo, &hi);
+    return hi > lo ? (hi + KT - 1) / KT - lo / KT : 0;
+}
+
+// A share's pieces, in order.
+struct Piece {
+    int b, g, qt;
+    Req r;
+    int lo, hi;          // the unit's keys
+    int t0, nt;          // first key tile (of KT keys) and number of tiles
+    bool whole;          // the unit's only piece: the output is written directly
+    int slot;            // else the slot of its partial result
+    int index;           // pieces with tiles before it in this share
+};
+template <int KT>
+struct Walk {
+    int b, g, qt, x, c, index;
+    int64_t rem;
+    bool first, have;
+    Req r;
+    __device__ __forceinline__ Walk(const Params& P, int cta) {
+        const Share s = P.shares[cta];
+        b = s.b; g = s.g; qt = s.qt; x = s.x; rem = s.len; c = cta; index = 0; first = true; have = false;
+    }
+    __device__ __forceinline__ bool next(const Params& P, Piece* p) {
+        while (rem > 0) {
+            if (!have) {
+                r = load_req(P.a, b);
+                have = true;
+                if (r.n == 0) {                                // no unit here
+                    if (++b >= P.a.B) return false;
+                    g = qt = x = 0; have = false;
+                    continue;
+                }
+            }
+            int lo, hi;
+            unit_keys<KT>(P.a, r, P.tpu, qt, &lo, &hi);
+            const int nt = hi > lo ? (hi + KT - 1) / KT - lo / KT : 0;
+            const int cost = kUnitCost + nt;
+            const int x0 = x, x1 = (int)min((int64_t)cost, x0 + rem);
+            const int f0 = min(max(x0 - kUnitCost, 0), nt), f1 = min(max(x1 - kUnitCost, 0), nt);
+            p->b = b; p->g = g; p->qt = qt; p->r = r; p->lo = lo; p->hi = hi;
+            p->t0 = lo / KT + f0; p->nt = f1 - f0;
+            p->whole = f1 - f0 == nt;
+            p->slot = 2 * c + (first ? 0 : 1);
+            p->index = index;
+            rem -= x1 - x0;
+            first = false;
+            if (x1 == cost) {
+                x = 0;
+                if ((qt + 1) * P.tpu >= r.n) {
+                    qt = 0;
+                    if (++g == P.a.nKv) { g = 0; ++b; have = false; if (b >= P.a.B) rem = 0; }
+                } else {
+                    ++qt;
+                }
+            } else {
+                x = x1;
+            }
+            if (f1 > f0) { ++index; return true; }
+            if (nt == 0 && x1 == cost) return true;         // no keys: zeros to write
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------------ plan
+// One block: the requests' costs and their prefix sums, then thread c places share c.
+template <int KT>
+__global__ void __launch_bounds__(kPlanThreads) attend_paged_plan_kernel(Params P) {
+    extern __shared__ int64_t s_pre[];                  // [B + 1] cost of the requests before b
+    __shared__ int64_t s_buf[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, B = P.a.B;
+    pdl_trigger();
+    pdl_wait();
+    // a request's cost: a thread per request for few units each, a warp for many
+    const bool by_warp = P.a.max_new > 4 * P.tpu;
+    for (int b = by_warp ? wid : tid; b < B; b += by_warp ? kPlanThreads / 32 : kPlanThreads) {
+        const Req r = load_req(P.a, b);
+        int64_t cost = 0;
+        const int units = (r.n + P.tpu - 1) / P.tpu;
+        for (int qt = by_warp ? lane : 0; qt < units; qt += by_warp ? 32 : 1)
+            cost += kUnitCost + unit_tiles<KT>(P.a, r, P.tpu, qt);
+        if (by_warp) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+        }
+        if (!by_warp || lane == 0) {
+            s_pre[b] = cost;
+            if (P.a.kv_len[b] != r.L || P.a.cu[b] != r.t0 || P.a.cu[b + 1] != r.t0 + r.n) atomicOr(P.status, DSPARK_DEV_BAD_LENGTH);
+        }
+    }
+    __syncthreads();
+    // exclusive prefix sums, a contiguous run of requests per thread
+    const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += s_pre[b] * P.a.nKv;
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_buf[wid] = inc;
+    __syncthreads();
+    int64_t base = 0, W = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < wid) base += s_buf[w];
+        W += s_buf[w];
+    }
+    base += inc - mine;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t cb = s_pre[b] * P.a.nKv;
+        s_pre[b] = base;
+        base += cb;
+    }
+    if (tid == 0) s_pre[B] = W;
+    __syncthreads();
+    // shares of at least kUnitCost + 1: below that a piece is all fixed work
+    const int64_t G = min((int64_t)kGrid, max((int64_t)1, W / (kUnitCost + 1)));
+    auto start = [&](int64_t c) { return c >= G ? W : W * c / G; };
+    if (tid >= kGrid) return;
+    const int64_t lo = start(tid), hi = start(tid + 1);
+    Share s{0, 0, 0, 0, hi - lo};
+    MergeUnit mu{0, 0, 0, 0, 0, -1};
+    if (hi > lo) {
+        int l = 0, h = B;                                // the last request that starts at or before lo and is not empty
+        while (h - l > 1) {
+            const int mid = (l + h) >> 1;
+            if (s_pre[mid] <= lo) l = mid; else h = mid;
+        }
+        const Req r = load_req(P.a, l);
+        const int64_t cg = (s_pre[l + 1] - s_pre[l]) / P.a.nKv;
+        int64_t rest = lo - s_pre[l];
+        s.b = l;
+        s.g = (int)(rest / cg);
+        rest -= s.g * cg;
+        int qt = 0, cost;
+        for (;; ++qt) {
+            cost = kUnitCost + unit_tiles<KT>(P.a, r, P.tpu, qt);
+            if (rest < cost) break;
+            rest -= cost;
+        }
+        s.qt = qt;
+        s.x = (int)rest;
+        // the cut at lo splits the unit's tiles, and is the first that does: this thread lists the unit
+        const int64_t u0 = lo - rest;                    // where the unit starts
+        if (tid > 0 && s.x > kUnitCost && start(tid - 1) - u0 <= kUnitCost) {
+            mu.b = s.b; mu.g = s.g; mu.qt = qt;
+            mu.c0 = tid - 1;
+            mu.odd = start(tid - 1) < u0;                // not the first region of that share
+            int c1 = tid;
+            while (c1 + 1 < G && start(c1 + 1) < u0 + cost) ++c1;
+            mu.c1 = c1;
+        }
+    }
+    P.shares[tid] = s;
+    P.merges[tid] = mu;
+}
+
+// ------------------------------------------------------------------ PTX used here alone
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T> __host__ __device__ constexpr uint32_t idesc(int M, int N, int b_mn_major);
+template <> __host__ __device__ constexpr uint32_t idesc<__half>(int M, int N, int mn) { return idesc_f16(M, N, mn); }
+template <> __host__ __device__ constexpr uint32_t idesc<__nv_bfloat16>(int M, int N, int mn) {
+    return idesc_bf16(M, N) | (uint32_t(mn) << 16);
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int HD_, int NQ_, int KT_, bool QTMEM_>
+struct Cfg {
+    static constexpr int HD = HD_, NQ = NQ_, KT = KT_;
+    static constexpr bool QTMEM = QTMEM_;                     // Q in tensor memory (staged through ring slots)
+    static constexpr int NCH = HD / 64;                       // 64-dimension chunks
+    static constexpr int kChunk = kRows * 128;                // a chunk of a query tile
+    static constexpr int kTile = KT * HD * 2;                 // a K or V tile
+    static constexpr int kQBytes = QTMEM ? 0 : NQ * NCH * kChunk;
+    static constexpr int kSlotsFit = (int)((kSmemMax - 1024 - 512 - kQBytes) / kTile);
+    static constexpr int NS = kSlotsFit < 12 ? kSlotsFit : 12;
+    static constexpr int kQPerSlot = kTile / kChunk;          // staged query chunks per slot
+    static constexpr int kQSlots = QTMEM ? (NCH + kQPerSlot - 1) / kQPerSlot : 0;
+    static constexpr int kSoft = NQ * 128;                    // softmax threads
+    static constexpr int kThreads = kSoft + 96;
+    static constexpr int kOCol = 2 * KT, kQCol = 2 * KT + HD; // TMEM columns: S buffers, O tiles, Q
+    static constexpr size_t kSmem = 1024 + kQBytes + (size_t)NS * kTile + 512;
+    static_assert(kSmem <= kSmemMax, "shared memory");
+    static_assert(2 * KT + NQ * HD + (QTMEM ? HD / 2 : 0) <= 512, "tensor memory");
+};
+
+struct Bars {
+    uint64_t full[12], free_[12], vissued[12], vready[12];
+    uint64_t sdone[2], pready[2], odone[2];
+    uint64_t qfull, qfree, spare;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// Ring entries before tile t's K and V within a piece of nt tiles: the order the MMAs take them in.
+template <int NQ> __device__ __forceinline__ int k_entry(int t) { return NQ == 2 ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+template <int NQ> __device__ __forceinline__ int v_entry(int t, int nt) {
+    return NQ == 2 ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2;
+}
+
+template <typename T, typename C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, Params P) {
+    constexpr int HD = C::HD, NQ = C::NQ, KT = C::KT, NCH = C::NCH, NS = C::NS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = base;                                       // [NQ][NCH][128 rows x 128 B]
+    uint8_t* ring = base + C::kQBytes;                        // NS tiles, [NCH][KT rows x 128 B]
+    Bars& B = *reinterpret_cast<Bars*>(ring + (size_t)NS * C::kTile);
+    volatile int* abort_flag = &B.abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kLoadWarp = NQ * 4, kMmaWarp = NQ * 4 + 1, kFixWarp = NQ * 4 + 2;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) { mbar_init(&B.full[i], 1); mbar_init(&B.free_[i], 1); mbar_init(&B.vissued[i], 1); mbar_init(&B.vready[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&B.sdone[i], 1); mbar_init(&B.pready[i], 128); mbar_init(&B.odone[i], 1); }
+        mbar_init(&B.qfull, C::QTMEM ? 128 : 1);
+        mbar_init(&B.qfree, 1);
+        mbar_init(&B.spare, 1);
+        B.abort = 0;
+        mbar_fence_init();
+        prefetch_tmap(&tmQ); prefetch_tmap(&tmK); prefetch_tmap(&tmV);
+    }
+    if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem;
+    pdl_wait();
+
+    Walk<KT> walk(P, blockIdx.x);
+    Piece p;
+    int e = 0;                                                // ring entries before the piece
+    int gs = 0;                                               // steps before the piece
+    bool ok = true;
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ loads
+        const int box = min(P.a.page_size, KT), per_tile = KT / box;
+        const int sub = lane / NCH, ch = lane % NCH;          // this lane's request of a tile: box `sub`, chunk `ch`
+        auto acquire = [&](int entry) {                       // the slot's previous tile has been read
+            const int s = entry % NS;
+            if (entry >= NS && !__all_sync(0xffffffffu, mbar_wait(&B.free_[s], (uint32_t)(entry / NS - 1) & 1u, abort_flag, P.status)))
+                return false;
+            return true;
+        };
+        int issued = 0;
+        while (ok && walk.next(P, &p)) {
+            if (p.nt == 0) continue;
+            const int tok = p.r.t0 + p.qt * P.tpu;
+            const uint32_t qbytes = (uint32_t)(P.tpt * P.a.grp * 128);
+            if (C::QTMEM) {
+                for (int s = 0; s < C::kQSlots && ok; ++s) {
+                    if (!acquire(e)) { ok = false; break; }
+                    if (lane == 0) {
+                        const int c0 = s * C::kQPerSlot, c1 = min(NCH, c0 + C::kQPerSlot);
+                        mbar_arrive_expect_tx(&B.full[e % NS], qbytes * (c1 - c0));
+                        for (int c = c0; c < c1; ++c)
+                            tma_load_4d(ring + (size_t)(e % NS) * C::kTile + (c - c0) * C::kChunk, &tmQ, &B.full[e % NS], c * 64, 0, p.g, tok);
+                    }
+                    ++e;
+                    issued = e;
+                }
+            } else {
+                if (p.index > 0 && !__all_sync(0xffffffffu, mbar_wait(&B.qfree, (uint32_t)(p.index - 1) & 1u, abort_flag, P.status))) { ok = false; break; }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&B.qfull, qbytes * NQ * NCH);
+                    for (int q = 0; q < NQ; ++q)
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_4d(sQ + (q * NCH + c) * C::kChunk, &tmQ, &B.qfull, c * 64, 0, p.g, tok + q * P.tpt);
+                }
+            }
+            // tile t's pages; boxes without a key of the unit are not loaded
+            const int32_t* table = P.a.table + (int64_t)p.b * P.a.max_pages;
+            auto page_of = [&](int t) {
+                const int key = (p.t0 + t) * KT + sub * box;
+                if (sub >= per_tile || t >= p.nt || key >= p.hi || key + box <= p.lo) return -2;
+                int page = table[key >> P.page_shift];
+                if (page < 0 || page >= P.a.num_pages) {
+                    atomicOr(P.status, DSPARK_DEV_BAD_PAGE);
+                    page = P.a.num_pages;                      // out of range: reads as zeros
+                }
+                return page;
+            };
+            auto load = [&](const CUtensorMap* m, bool v, int t, int page) {
+                if (!acquire(e)) return false;
+                const int s = e % NS;
+                const unsigned act = __ballot_sync(0xffffffffu, page != -2);
+                const int k0 = (p.t0 + t) * KT;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&B.full[s], (uint32_t)__popc(act) * (uint32_t)(box * 128));
+                    if (v && (k0 < p.lo || k0 + KT > p.hi)) mbar_arrive(&B.vissued[s]);
+                }
+                __syncwarp();
+                if (page != -2) {
+                    const int key = k0 + sub * box;
+                    tma_load_4d(ring + (size_t)s * C::kTile + ch * (KT * 128) + sub * (box * 128), m, &B.full[s], ch * 64, p.g,
+                                key & (P.a.page_size - 1), page);
+                }
+                ++e;
+                issued = e;
+                return true;
+            };
+            int cur = page_of(0), prev = cur;
+            for (int t = 0; t < p.nt && ok; ++t) {
+                const int nxt = page_of(t + 1);                // in flight while this tile waits for its slot
+                ok = load(&tmK, false, t, cur);
+                if (NQ == 2) ok = ok && load(&tmV, true, t, cur);
+                else if (t > 0) ok = ok && load(&tmV, true, t - 1, prev);
+                prev = cur;
+                cur = nxt;
+            }
+            if (NQ == 1 && ok) ok = load(&tmV, true, p.nt - 1, prev);
+        }
+        if (!ok) {                                            // copies in flight land before the block ends (bounded)
+            const uint64_t deadline = global_timer_ns() + kWaitLimitNs;
+            bool in = true;
+            for (int i = max(0, issued - NS); i < issued && in; ++i)
+                in = mbar_wait_until(&B.full[i % NS], (uint32_t)(i / NS) & 1u, deadline);
+            if (!C::QTMEM && in && p.index >= 0) mbar_wait_until(&B.qfull, (uint32_t)p.index & 1u, global_timer_ns() + 1000000ull);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMAs (one thread)
+        if (lane == 0) {
+            uint32_t vpar = 0;                                // parity of each slot's next vready phase
+            constexpr uint32_t id_qk = idesc<T>(kRows, KT, 0), id_pv = idesc<T>(kRows, HD, 1);
+            while (ok && walk.next(P, &p)) {
+                if (p.nt == 0) continue;
+                const int e0 = e + C::kQSlots, ns = p.nt * NQ;
+                if (!mbar_wait(&B.qfull, (uint32_t)p.index & 1u, abort_flag, P.status)) { ok = false; break; }
+                for (int s = 0; s < C::kQSlots; ++s) mbar_arrive(&B.free_[(e + s) % NS]);
+                auto issue_s = [&](int s) {
+                    const int t = s / NQ, q = s % NQ, en = e0 + k_entry<NQ>(t), sl = en % NS, buf = (gs + s) & 1;
+                    if (q == 0 && !mbar_wait(&B.full[sl], (uint32_t)(en / NS) & 1u, abort_flag, P.status)) return false;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(buf * KT);
+                    const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)sl * C::kTile));
+                    if (C::QTMEM) {
+#pragma unroll
+                        for (int j = 0; j < HD / 16; ++j)
+                            mma_f16_ts(d, tmem + (uint32_t)(C::kQCol + 8 * j), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
+                    } else {
+                        const uint64_t ad = sdesc_k_sw128(smem_u32(sQ + q * NCH * C::kChunk));
+#pragma unroll
+                        for (int j = 0; j < HD / 16; ++j)
+                            mma_bf16(d, ad + (uint64_t)(((j >> 2) * C::kChunk + (j & 3) * 32) >> 4), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
+                    }
+                    mma_commit(&B.sdone[buf]);
+                    if (q == NQ - 1) mma_commit(&B.free_[sl]);
+                    if (!C::QTMEM && s == ns - 1) mma_commit(&B.qfree);
+                    return true;
+                };
+                if (!issue_s(0) || (ns > 1 && !issue_s(1))) { ok = false; break; }
+                for (int s = 0; s < ns; ++s) {
+                    const int t = s / NQ, q = s % NQ, en = e0 + v_entry<NQ>(t, p.nt), sl = en % NS, buf = (gs + s) & 1;
+                    if (q == 0) {
+                        const int k0 = (p.t0 + t) * KT;
+                        if (k0 < p.lo || k0 + KT > p.hi) {    // rows outside the unit's keys: zeroed first
+                            if (!mbar_wait(&B.vready[sl], (vpar >> sl) & 1u, abort_flag, P.status)) { ok = false; break; }
+                            vpar ^= 1u << sl;
+                        } else if (!mbar_wait(&B.full[sl], (uint32_t)(en / NS) & 1u, abort_flag, P.status)) { ok = false; break; }
+                    }
+                    if (!mbar_wait(&B.pready[buf], (uint32_t)((gs + s) >> 1) & 1u, abort_flag, P.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(C::kOCol + q * HD), pa = tmem + (uint32_t)(buf * KT);
+                    const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)sl * C::kTile), KT * 128);
+#pragma unroll
+                    for (int j = 0; j < KT / 16; ++j)
+                        mma_f16_ts(d, pa + (uint32_t)(8 * j), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
+                    mma_commit(&B.odone[buf]);
+                    if (q == NQ - 1) mma_commit(&B.free_[sl]);
+                    if (s + 2 < ns && !issue_s(s + 2)) { ok = false; break; }
+                }
+                e = e0 + 2 * p.nt;
+                gs += ns;
+            }
+            if (!ok) {                                        // MMAs in flight end first (bounded)
+                mma_commit(&B.spare);
+                if (!mbar_wait_until(&B.spare, 0u, global_timer_ns() + kWaitLimitNs)) atomicOr(P.status, DSPARK_DEV_WAIT_TIMEOUT);
+            }
+        }
+    } else if (warp == kFixWarp) {
+        // ------------------------------------------------------------ V rows outside the unit's keys
+        // (this warp skips entries, so a slot's load is first known to be issued: only then does the
+        // parity of its full barrier name this load)
+        uint32_t vpar = 0;
+        while (ok && walk.next(P, &p)) {
+            if (p.nt == 0) continue;
+            const int e0 = e + C::kQSlots;
+            for (int t = 0; t < p.nt; ++t) {
+                const int k0 = (p.t0 + t) * KT, a = max(0, p.lo - k0), b = min(KT, p.hi - k0);   // rows [a, b) stay
+                if (a == 0 && b == KT) continue;
+                const int en = e0 + v_entry<NQ>(t, p.nt), sl = en % NS;
+                const bool in = mbar_wait(&B.vissued[sl], (vpar >> sl) & 1u, abort_flag, P.status) &&
+                                mbar_wait(&B.full[sl], (uint32_t)(en / NS) & 1u, abort_flag, P.status);
+                vpar ^= 1u << sl;
+                if (!__all_sync(0xffffffffu, in)) { ok = false; break; }
+                uint8_t* tile = ring + (size_t)sl * C::kTile;
+                const int dead = KT - (b - a);
+                for (int i = lane; i < NCH * dead * 8; i += 32) {
+                    const int c = i / (dead * 8), rest = i - c * (dead * 8), row = rest >> 3;
+                    *reinterpret_cast<uint4*>(tile + c * (KT * 128) + (row < a ? row : row - a + b) * 128 + (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_shared();                         // the MMAs read through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.vready[sl]);
+            }
+            e = e0 + 2 * p.nt;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax: one thread per query row
+        const int q = NQ == 2 ? tid >> 7 : 0, r = tid & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tO = tmem + (uint32_t)(C::kOCol + q * HD) + lane_off;
+        const float c = P.a.scale * 1.4426950408889634f;      // scores to log2
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
+        };
+        const int grp = P.a.grp, tok_r = r / grp, head_r = r - tok_r * grp;
+        while (ok && walk.next(P, &p)) {
+            const int i = p.qt * P.tpu + q * P.tpt + tok_r;   // this row's token of the request
+            const bool valid = tok_r < P.tpt && i < p.r.n;
+            const int pos = p.r.L - p.r.n + i;
+            const int row_hi = P.a.causal ? min(p.r.L, pos + 1) : p.r.L;
+            const int row_lo = P.a.window > 0 ? max(0, pos - P.a.window + 1) : 0;
+            // keys that every row of the tile sees (tokens of the whole query tile)
+            const int i_first = p.qt * P.tpu + q * P.tpt, i_last = min(p.r.n, i_first + P.tpt) - 1;
+            const int all_hi = P.a.causal ? min(p.r.L, p.r.L - p.r.n + i_first + 1) : p.r.L;
+            const int all_lo = P.a.window > 0 ? max(0, p.r.L - p.r.n + i_last - P.a.window + 1) : 0;
+            float m = -INFINITY, l = 0.f;
+            if (C::QTMEM && p.nt > 0) {
+                // the staged query rows into tensor memory, two 16-bit values per column; the S products of
+                // the piece before have all completed (their last was waited for)
+                const bool live = r < P.tpt * grp;
+                for (int s = 0; s < C::kQSlots && ok; ++s) {
+                    const int en = e + s, sl = en % NS;
+                    if (!wait(&B.full[sl], (uint32_t)(en / NS) & 1u)) { ok = false; break; }
+                    const int c0 = s * C::kQPerSlot, c1 = min(NCH, c0 + C::kQPerSlot);
+                    for (int cc = c0; cc < c1; ++cc) {
+                        const uint8_t* line = ring + (size_t)sl * C::kTile + (cc - c0) * C::kChunk + r * 128;
+#pragma unroll
+                        for (int j0 = 0; j0 < 8; j0 += 4) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                                if (live) u = *reinterpret_cast<const uint4*>(line + (((j0 + j) ^ (r & 7)) * 16));
+                                w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+                            }
+                            tmem_st_x16(tmem + (uint32_t)(C::kQCol + cc * 32 + j0 * 4) + lane_off, w);
+                        }
+                    }
+                }
+                if (!ok) break;
+                tmem_st_wait();
+                fence_async_shared();                         // reads done before the slots are loaded again
+                tc_fence_before();
+                mbar_arrive(&B.qfull);                        // the MMA thread then frees the slots
+            }
+            int last_step = -1;
+            for (int t = 0; t < p.nt; ++t) {
+                const int st = gs + t * NQ + q, buf = st & 1;
+                const uint32_t tS = tmem + (uint32_t)(buf * KT) + lane_off;
+                if (!wait(&B.sdone[buf], (uint32_t)(st >> 1) & 1u)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t u[KT];
+#pragma unroll
+                for (int j = 0; j < KT; j += 32) tmem_ld_x32(tS + (uint32_t)j, u + j);
+                tmem_ld_wait();
+                const int k0 = (p.t0 + t) * KT;
+                if (k0 < all_lo || k0 + KT > all_hi) {        // some row does not see some key
+                    const int a = row_lo - k0, b = row_hi - k0;
+#pragma unroll
+                    for (int j = 0; j < KT; ++j)
+                        if (j < a || j >= b) u[j] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(u[j]);
+#pragma unroll
+                for (int j = 4; j < KT; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(u[j]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool need = m > -INFINITY && top > m + kRescale;
+                if (__any_sync(0xffffffffu, need)) {
+                    // O holds the tiles before at the old maximum: their PV must have landed
+                    if (!wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                    const float f = need ? ex2(m - top) : 1.f;
+                    if (need) { l *= f; m = top; }
+#pragma unroll
+                    for (int d = 0; d < HD; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(tO + (uint32_t)d, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st_x16(tO + (uint32_t)d, o);
+                    }
+                    tmem_st_wait();
+                }
+                if (m == -INFINITY) m = top;                  // nothing summed yet
+                const float neg = m == -INFINITY ? 0.f : -m;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < KT; j += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int jj = 0; jj < 32; jj += 2) {
+                        const float p0 = ex2(fmaf(__uint_as_float(u[j + jj]), c, neg)), p1 = ex2(fmaf(__uint_as_float(u[j + jj + 1]), c, neg));
+                        ls[(jj >> 1) & 3] += p0 + p1;
+                        w[jj >> 1] = pack2<T>(p0, p1);
+                    }
+                    tmem_st_x16(tS + (uint32_t)(j / 2), w);
+                }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&B.pready[buf]);
+                last_step = st;
+            }
+            if (!ok) break;
+            // ---- the piece's result
+            if (p.nt > 0 && !wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u)) { ok = false; break; }
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int64_t tok = p.r.t0 + i;
+            const int h = p.g * grp + head_r;
+            if (p.whole) {
+                T* out = static_cast<T*>(P.a.out) + tok * P.a.out_stride + (int64_t)h * HD;
+#pragma unroll
+                for (int d = 0; d < HD; d += 32) {
+                    uint32_t o[32];
+                    if (p.nt > 0) {
+                        tmem_ld_x32(tO + (uint32_t)d, o);
+                        tmem_ld_wait();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = l > 0.f ? pack2<T>(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv) : 0u;
+                            *reinterpret_cast<uint4*>(out + d + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (valid && P.a.lse) P.a.lse[tok * P.a.nH + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            } else {
+                const int64_t row = (int64_t)p.slot * (NQ * kRows) + q * kRows + r;
+                if (valid) *reinterpret_cast<float2*>(P.part_ml + row * 2) = make_float2(l > 0.f ? m : -INFINITY, l);
+#pragma unroll
+                for (int d = 0; d < HD; d += 32) {
+                    uint32_t o[32];
+                    tmem_ld_x32(tO + (uint32_t)d, o);
+                    tmem_ld_wait();
+                    if (valid) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(P.part_o + row * HD + d + j) =
+                                make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv, __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                    }
+                }
+            }
+            tc_fence_before();                                // O read before the next piece's first PV (behind its P)
+            if (p.nt > 0) {
+                e += C::kQSlots + 2 * p.nt;
+                gs += p.nt * NQ;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ merge
+// out = sum_s w_s O_s / sum_s w_s, w_s = l_s exp2(m_s - M), over a unit's pieces in order: one warp per row.
+constexpr int kMergeWarps = 8;
+template <typename T, int HD, int NQ>
+__global__ void __launch_bounds__(kMergeWarps * 32) attend_paged_merge_kernel(Params P) {
+    constexpr int PER = HD / 32;
+    pdl_trigger();
+    pdl_wait();
+    const MergeUnit u = P.merges[blockIdx.x];
+    if (u.c1 < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rr = blockIdx.y * kMergeWarps + warp, q = rr / kRows, r = rr % kRows;
+    const Req req = load_req(P.a, u.b);
+    const int tr = r / P.a.grp, i = u.qt * P.tpu + q * P.tpt + tr;
+    if (tr >= P.tpt || i >= req.n) return;
+    const int h = u.g * P.a.grp + r - tr * P.a.grp, n = u.c1 - u.c0 + 1;
+    auto row_of = [&](int s) { return (int64_t)(s == 0 ? 2 * u.c0 + u.odd : 2 * (u.c0 + s)) * (NQ * kRows) + rr; };
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32) M = fmaxf(M, P.part_ml[row_of(s) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[PER], den = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+    for (int s = 0; s < n; ++s) {
+        const float2 ml = *reinterpret_cast<const float2*>(P.part_ml + row_of(s) * 2);
+        const float w = ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
+        den += w;
+        const float* o = P.part_o + row_of(s) * HD + lane;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] = fmaf(w, o[32 * k], acc[k]);
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    T* out = static_cast<T*>(P.a.out) + (int64_t)(req.t0 + i) * P.a.out_stride + (int64_t)h * HD + lane;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) out[32 * k] = from_f<T>(acc[k] * inv);
+    if (P.a.lse && lane == 0) P.a.lse[(int64_t)(req.t0 + i) * P.a.nH + h] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
+std::once_flag g_enc_once;
+
+bool make_map(CUtensorMap* tm, const void* ptr, int dtype, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+    std::call_once(g_enc_once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!g_enc) return false;
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_enc(tm, dtype == DSPARK_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                 const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout { size_t status, shares, merges, ml, o, total; };
+Layout layout(int hd) {
+    const int rows = hd <= 128 ? 2 * kRows : kRows;
+    Layout l{};
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
+    l.status = take(4);
+    l.shares = take(kGrid * sizeof(Share));
+    l.merges = take(kGrid * sizeof(MergeUnit));
+    l.ml = take((size_t)2 * kGrid * rows * 2 * sizeof(float));
+    l.o = take((size_t)2 * kGrid * rows * hd * sizeof(float));
+    l.total = at;
+    return l;
+}
+
+template <typename T, typename C>
+cudaError_t launch(Params P, cudaStream_t s) {
+    const PagedAttn& a = P.a;
+    P.tpt = kRows / a.grp;
+    P.tpu = C::NQ * P.tpt;
+    CUtensorMap tq, tk, tv;
+    const cuuint64_t hb = (cuuint64_t)a.hd * 2;
+    const cuuint64_t qd[4] = {(cuuint64_t)a.hd, (cuuint64_t)a.grp, (cuuint64_t)a.nKv, (cuuint64_t)a.T};
+    const cuuint64_t qs[3] = {hb, hb * a.grp, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)a.grp, 1, (cuuint32_t)P.tpt};
+    const cuuint64_t kd[4] = {(cuuint64_t)a.hd, (cuuint64_t)a.nKv, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages};
+    const cuuint64_t ks[3] = {hb, hb * a.nKv, hb * a.nKv * a.page_size};
+    const cuuint32_t kb[4] = {64, 1, (cuuint32_t)std::min(a.page_size, C::KT), 1};
+    if (!make_map(&tq, a.q, a.dtype, qd, qs, qb) || !make_map(&tk, a.k, a.dtype, kd, ks, kb) || !make_map(&tv, a.v, a.dtype, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    auto kern = attend_paged_tc_kernel<T, C>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attend_paged_plan_kernel<C::KT>, dim3(1), dim3(kPlanThreads), (a.B + 1) * sizeof(int64_t), s, P);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(kGrid), dim3(C::kThreads), C::kSmem, s, tq, tk, tv, P);
+    if (e == cudaSuccess)
+        e = launch_pdl(attend_paged_merge_kernel<T, C::HD, C::NQ>, dim3(kGrid, C::NQ * kRows / kMergeWarps), dim3(kMergeWarps * 32), 0, s, P);
+    return e;
+}
+
+template <typename T>
+cudaError_t dispatch(const Params& P, cudaStream_t s) {
+    // two query tiles per unit once a request's rows fill more than one: K and V tiles then feed twice the
+    // MMAs and the softmax of one tile overlaps the MMAs of the other
+    const bool two = (int64_t)P.a.max_new * P.a.grp > kRows;
+    switch (P.a.hd) {
+        case 64: return two ? launch<T, Cfg<64, 2, 128, false>>(P, s) : launch<T, Cfg<64, 1, 128, false>>(P, s);
+        case 128: return two ? launch<T, Cfg<128, 2, 128, false>>(P, s) : launch<T, Cfg<128, 1, 128, false>>(P, s);
+        case 192: return launch<T, Cfg<192, 1, 64, true>>(P, s);
+        default: return launch<T, Cfg<256, 1, 64, true>>(P, s);
+    }
+}
+
+}  // namespace
+
+bool attend_paged_tc_supported(const dspark_paged_cache& c, int n_heads) {
+    return c.dtype != DSPARK_DTYPE_F32 && c.head_dim % 64 == 0 && c.page_size >= 8 && (c.page_size & (c.page_size - 1)) == 0 &&
+           n_heads / c.n_kv <= kRows && (int64_t)c.page_size * c.n_kv * c.head_dim * 2 < ((int64_t)1 << 40);
+}
+int attend_paged_max_batch() { return kMaxBatch; }
+size_t attend_paged_tc_workspace(int hd) { return layout(hd).total; }
+
+cudaError_t launch_attend_paged_tc(const PagedAttn& a, void* ws, cudaStream_t s) {
+    const Layout l = layout(a.hd);
+    char* w = static_cast<char*>(ws);
+    Params P{};
+    P.a = a;
+    P.shares = reinterpret_cast<Share*>(w + l.shares);
+    P.merges = reinterpret_cast<MergeUnit*>(w + l.merges);
+    P.part_ml = reinterpret_cast<float*>(w + l.ml);
+    P.part_o = reinterpret_cast<float*>(w + l.o);
+    P.status = a.status ? a.status : reinterpret_cast<int32_t*>(w + l.status);
+    while ((1 << P.page_shift) < a.page_size) ++P.page_shift;
+    return a.dtype == DSPARK_DTYPE_F16 ? dispatch<__half>(P, s) : dispatch<__nv_bfloat16>(P, s);
+}
+
+}  // namespace tc
+}  // namespace dspark

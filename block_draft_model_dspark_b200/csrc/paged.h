@@ -28,6 +28,10 @@ __device__ __forceinline__ void set_status(int32_t* status, int32_t bits) {
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
+// The longest request an attention call takes: with it every key index and window edge fits 32 bits
+// (2^30 keys of the smallest head are more than the GPU's memory).
+constexpr int kMaxKeys = 1 << 30;
+
 // Attention over a paged cache: what both kernels take.
 struct PagedAttn {
     const void* q; void* out; float* lse;             // q, out [T][nH][hd] with row strides; lse [T][nH] or NULL
@@ -41,5 +45,11 @@ struct PagedAttn {
     int causal, window;
 };
 cudaError_t launch_attend_paged_simt(const PagedAttn& a, cudaStream_t s);
+namespace tc {
+bool attend_paged_tc_supported(const dspark_paged_cache& c, int n_heads);
+int attend_paged_max_batch();
+size_t attend_paged_tc_workspace(int hd);
+cudaError_t launch_attend_paged_tc(const PagedAttn& a, void* ws, cudaStream_t s);
+}  // namespace tc
 
 }  // namespace dspark
