@@ -510,7 +510,8 @@ int dspark_attend_paged(const dspark_paged_cache* cache, int32_t layer, const vo
  *   probs   device float [rows] or NULL: the token's share of the kept weight
  *   ws      >= dspark_sample_workspace_bytes(rows, vocab), 256-byte aligned; calls that may
  *           overlap on the GPU need one each
- * Weights and their sums are formed in 64 bits; a weight below 2^-62 of their sum counts as 0. vocab <= 2^24.
+ * Weights are within 2^-45 and summed in 64 bits; one below 2^-79 of the largest counts as 0 (such a
+ * candidate is not drawn). vocab <= 2^24, rows <= 2^26.
  */
 size_t dspark_sample_workspace_bytes(int32_t rows, int32_t vocab);
 int dspark_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t rows, int32_t vocab, const float* u,
