@@ -8,22 +8,27 @@
 // index i (in the vocabulary's order) whose cumulative kept mass exceeds
 // u times the total.
 //
-// A cluster of C CTAs owns a row, a contiguous slice each, kept in shared memory: the row
-// is read from HBM once, every later pass reads shared memory, and the CTAs exchange a few numbers
-// through distributed shared memory. A filter's boundary is found from a
-// histogram over (m - x) / T, linear bins of 1/64 (as many elements a bin as
-// the density has there: the adds rarely collide), restricted to elements that
-// can matter: for top-k those not below the smallest of k thread groups' maxima,
-// for top-p those with a weight above (1 - p) / V (the others together weigh less than
-// 1 - p of the total). If the elements down to the boundary fit a list of 1024,
-// one CTA sorts it and finishes the row alone, the others leave. Else the
-// boundary's bins are split 2048 ways once more and only the elements of the bins that
-// still may hold it are sorted; what overflows even that (many equal logits) is bisected.
+// A cluster of C CTAs owns a row, a contiguous slice each, and the CTAs exchange a few numbers
+// through distributed shared memory: C = 1 when the rows alone fill the GPU (each pass then streams
+// the row), more for fewer rows (a slice that fits is kept in shared memory). The first pass finds the maximum, and
+// for rows whose total is needed the sum at the same time, relative to the thread's own running
+// maximum. An unfiltered row then only looks into the piece of it that holds the token.
+//
+// top-k: the k-th largest of the threads' maxima is at most the k-th largest
+// entry; the few entries at or above it (only threads whose maximum is look
+// again) are listed, sorted and finished by one CTA, the others leave.
+// top-p: a histogram over (m - x) / T in linear bins of 1/64 (as many elements a bin as
+// the density has there: the adds rarely collide) of the entries with a weight above
+// (1 - p) / V (the others together weigh less than 1 - p of the total). A bin also sums its
+// elements' places within it: with their mean z its mass lies between n e^-z (Jensen) and n e^-z
+// e^(h^2 / 8) (Hoeffding; h = 1/64), which leaves a bin or two for the prefix's end. If all entries down to
+// there fit the list, one CTA finishes the row; else only those bins are listed, with the exact
+// mass above them. What overflows the list (thousands of equal logits) is bisected.
 //
 // Weights and sums are 64-bit: in a flat tail a token's share is about 10^-7 of the mass,
 // so 32-bit sums would move the drawn token. exp is 2^(k/16) from a table (16 doubles: no two
 // of them share a bank) times the Taylor polynomial of degree 6 on |r| <= 1/32 octave, within
-// 2^-46; 12 64-bit operations an element, which is what bounds unfiltered rows.
+// 2^-46: 12 64-bit operations an element.
 #include <algorithm>
 #include <cfloat>
 
@@ -33,14 +38,15 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kList = 1024;
+constexpr int NT = 512;                              // threads; two CTAs an SM
+constexpr int kWarps = NT / 32;
+constexpr int kBins = 1024;
+constexpr int kList = 4096;
 constexpr int kMaxCluster = 16;
 constexpr float kPerUnit = 64.f;                     // bins per unit of (m - x) / T
-constexpr size_t kHeadBytes = 8192;                  // the histogram, later the list
-constexpr double kSlack = 3e-5;                      // above the relative rounding of a bin and its edge's weight (32 bits, (m - x) / T up to 32)
+constexpr size_t kHeadBytes = kList * 8;             // the histogram, later the list
+constexpr double kSlack = 3e-5;                      // above the relative rounding of a bin and its edge's weight (32 bits, (m - x) / T up to 16)
+constexpr double kFixed = 2251799813685248.0;        // 2^51: sums of kList weights (at most 1) in 63 bits
 
 struct SampleParams {
     const void* logits; int64_t stride; int rows, V, cluster, slice, resident;
@@ -51,10 +57,11 @@ struct SampleParams {
 // Numbers that the CTAs of a cluster tell each other: slot r is rank r's.
 struct Exchange {
     uint64_t best[kMaxCluster];
-    double total[kMaxCluster], above[kMaxCluster], above2[kMaxCluster], kept[kMaxCluster];
-    double lo[kMaxCluster], up[kMaxCluster], cnt[kMaxCluster];          // of the rank's bins
+    double total[kMaxCluster], above[kMaxCluster], kept[kMaxCluster];
+    double lo[kMaxCluster], up[kMaxCluster], cnt[kMaxCluster], listed[kMaxCluster];
     double bis_mass[2][kMaxCluster], bis_cnt[2][kMaxCluster];
     uint64_t cut;
+    unsigned long long piece[kWarps];                // listed entries that stay, per warp's piece of the slice, in 1 / kFixed
     unsigned int n_list;
 };
 struct Scratch {
@@ -86,6 +93,10 @@ __device__ __forceinline__ uint32_t add_u32(unsigned int* p, int rank, uint32_t 
     return old;
 }
 
+__device__ __forceinline__ void add_u64(unsigned long long* p, int rank, uint64_t v) {
+    asm volatile("red.shared::cluster.add.u64 [%0], %1;" ::"r"(tc::mapa_shared(p, rank)), "l"(v) : "memory");
+}
+
 // ------------------------------------------------------------------ values
 // Bits in the order of the values (-0 as 0).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -100,25 +111,26 @@ __device__ __forceinline__ uint64_t rank_of(float x, int i) { return ((uint64_t)
 
 struct Weights {
     double m, c16;
-    float mf, cutoff, inv_t;
+    float mf, cutoff, range, z_scale;
     const double* tab;
-    __device__ __forceinline__ void set(float mx, float T, const double* t) {
-        mf = mx;
-        m = (double)mx;
+    __device__ __forceinline__ void set(float T, const double* t) {
         c16 = 16.0 * 1.4426950408889634073599 / (double)T;
-        inv_t = kPerUnit / T;
-        cutoff = mx == INFINITY ? mx : fmaxf(mx - 55.f * T, -FLT_MAX);   // weights below 2^-79 count as 0
+        z_scale = kPerUnit / T;
+        range = 55.f * T;                                                // weights below 2^-79 count as 0
         tab = t;
     }
-    __device__ __forceinline__ double operator()(float x) const {
-        if (!(x >= cutoff)) return 0.0;
-        if (x == mf) return 1.0;
+    __device__ __forceinline__ void at(float mx) {
+        mf = mx;
+        m = (double)mx;
+        cutoff = fmaxf(mx - range, -FLT_MAX);
+    }
+    // For x >= cutoff; any number for the others (NaN and -infinity among them).
+    __device__ __forceinline__ double raw(float x) const {
         const double magic = 6755399441055744.0;                         // 1.5 2^52: the sum's low word is the rounded integer
         const double d = (double)x - m, t = fma(d, c16, magic);
         const int k = __double2loint(t);
         const double r = fma(d, c16, -(t - magic));                      // |r| <= 1/2 sixteenth of an octave
-        // (ln 2 / 16)^n / n!
-        double p = 9.181219573844436e-12;
+        double p = 9.181219573844436e-12;                                // (ln 2 / 16)^n / n!
         p = fma(p, r, 1.271587195055813e-9);
         p = fma(p, r, 1.467610032291943e-7);
         p = fma(p, r, 1.3550807779497455e-5);
@@ -128,15 +140,11 @@ struct Weights {
         p *= tab[k & 15];
         return __hiloint2double(__double2hiint(p) + ((k >> 4) << 20), __double2loint(p));
     }
-    // (m - x) / T in bins, before rounding down; falls with x.
-    __device__ __forceinline__ float z(float x) const { return (mf - x) * inv_t; }
-    __device__ __forceinline__ int bin(float x) const { return min((int)fminf(z(x), 4096.f), kBins - 1); }
+    __device__ __forceinline__ double operator()(float x) const { return x >= cutoff ? raw(x) : 0.0; }
+    // m - x in bins, before rounding down; falls with x.
+    __device__ __forceinline__ float z(float x) const { return fminf((mf - x) * z_scale, 4096.f); }
+    __device__ __forceinline__ int bin(float x) const { return min((int)z(x), kBins - 1); }
 };
-
-template <typename X> __device__ __forceinline__ float clean(X v) {      // NaN counts as -infinity
-    const float x = to_f(v);
-    return x != x ? -INFINITY : x;
-}
 
 // ------------------------------------------------------------------ block helpers
 template <typename T, typename Op>
@@ -185,7 +193,7 @@ __device__ void sort_falling(uint64_t* a, int n) {
     __syncthreads();
     for (int k = 2; k <= n; k <<= 1) {
         for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int t = tid; t < n / 2; t += kThreads) {
+            for (int t = tid; t < n / 2; t += NT) {
                 const int i = 2 * t - (t & (j - 1));
                 const uint64_t x = a[i], y = a[i + j];
                 if ((x < y) == ((i & k) == 0)) { a[i] = y; a[i + j] = x; }
@@ -196,23 +204,44 @@ __device__ void sort_falling(uint64_t* a, int n) {
     __syncthreads();
 }
 
+// Adds the weights of a vector's entries >= thr that `pred` accepts; no branches, so that their 64-bit chains overlap.
+template <int VEC, typename Pred>
+__device__ __forceinline__ void add_mass(const Weights& W, const float (&x)[VEC], int i0, float thr, Pred pred, double& a, double& b) {
+    double w[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = W.raw(x[i]);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+        if (x[i] >= thr && pred(x[i], i0 + i, w[i])) a += w[i];
+        if (x[i + 1] >= thr && pred(x[i + 1], i0 + i + 1, w[i + 1])) b += w[i + 1];
+    }
+}
+
 template <typename X>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(SampleParams P) {
-    constexpr int VEC = 16 / (int)sizeof(X);
+__global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
+    constexpr int VEC = 16 / (int)sizeof(X), BATCH = 4;       // vectors in flight a thread
     extern __shared__ __align__(16) uint8_t smem[];
-    uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem);       // [kBins] elements
+    uint32_t* place = hist + kBins;                           // [kBins] their places in the bin, in 1/1024; then the mean as a float
     uint64_t* list = reinterpret_cast<uint64_t*>(smem);
     uint4* data = reinterpret_cast<uint4*>(smem + kHeadBytes);
     __shared__ Scratch S;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, C = P.cluster;
     const int rank = C > 1 ? (int)tc::cluster_ctarank() : 0, r = blockIdx.x / C;
-    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for before the first exchange
     if (tid == 0) S.x.n_list = 0;
+    if (tid < kWarps) S.x.piece[tid] = 0;
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for before the first exchange
     if (tid < 16) S.tab[tid] = exp2((double)tid * 0.0625);
     pdl_trigger();
     pdl_wait();
     const float T = P.temperature ? P.temperature[r] : 1.f, p = P.top_p ? P.top_p[r] : 1.f, mp = P.min_p ? P.min_p[r] : 0.f, u = P.u[r];
-    const int k_in = P.top_k ? P.top_k[r] : 0;
+    const int k = P.top_k ? P.top_k[r] : 0;
+    const bool alone = !(T > 0.f) || p <= 0.f || mp > 1.f || k == 1;                    // greedy, or a filter that leaves one
+    const bool has_p = p < 1.f, has_k = k > 0 && k < P.V;
+    const double low = mp > 0.f ? (double)mp : 0.0;
+    const bool sum_now = !alone && !has_k && (has_p || low == 0.0);                     // the whole row's mass is needed
+    Weights W;
+    W.set(T, S.tab);
 
     // The slice, counted from the 16-byte boundary at or before the row: element j of it is entry s0 + j - off.
     const X* row = static_cast<const X*>(P.logits) + (int64_t)r * P.stride;
@@ -233,16 +262,31 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(SampleParams P) {
         }
         return raw;
     };
-    // f(x, index) over vectors [a, b) of the slice, `step` apart
-    auto scan = [&](int a, int b, int step, auto f) {
-        for (int v = a; v < b; v += step) {
-            const uint4 raw = P.resident ? data[v] : fetch(v);
-            const X* e = reinterpret_cast<const X*>(&raw);
+    bool inf_max = false;                                      // the maximum is infinite: its candidates count as 0, the others as -infinity
+    auto value = [&](X e) {
+        const float x = to_f(e);
+        return !inf_max ? x : x == INFINITY ? 0.f : -INFINITY;
+    };
+    // f(x[VEC], index of the first, their maximum (a NaN loses)) over vectors [a, b) of the slice, `step` apart
+    auto scan = [&](int a, int b, int step, bool first, auto f) {
+        for (int v = a; v < b; v += BATCH * step) {
+            uint4 raw[BATCH];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f(clean(e[i]), s0 + v * VEC + i - off);
+            for (int q = 0; q < BATCH; ++q)
+                if (v + q * step < b) raw[q] = P.resident && !first ? data[v + q * step] : fetch(v + q * step);
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) {
+                if (v + q * step >= b) break;
+                if (P.resident && first) data[v + q * step] = raw[q];
+                const X* e = reinterpret_cast<const X*>(&raw[q]);
+                float x[VEC], hi = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) { x[i] = value(e[i]); hi = fmaxf(hi, x[i]); }
+                f(x, s0 + (v + q * step) * VEC - off, hi);
+            }
         }
     };
-    auto each = [&](auto f) { scan(v0 + lane, v1, 32, f); };   // over the slice, a contiguous piece per warp
+    auto each = [&](auto f) { scan(v0 + lane, v1, 32, false, f); };      // over the slice, a contiguous piece per warp
     auto meet = [&] { if (C > 1) cluster_sync(); else __syncthreads(); };
     auto tell = [&](auto* slots, auto v) { if (tid < C) put(&slots[rank], tid, v); };   // this rank's number, to every CTA
     auto sum_of = [&](const double* slots) {
@@ -250,374 +294,388 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(SampleParams P) {
         for (int q = 0; q < C; ++q) t += slots[q];
         return t;
     };
+    auto any = [](float, int, double) { return true; };
 
-    // ---------------------------------------------------------------- the slice, its maximum
+    // ---------------------------------------------------------------- the maximum, and the mass
     float best = -INFINITY;
-    int best_i = 0x7fffffff;
-    for (int v = v0 + lane; v < v1; v += 8 * 32) {
-        uint4 raw[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (v + 32 * q < v1) raw[q] = fetch(v + 32 * q);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (v + 32 * q >= v1) break;
-            if (P.resident) data[v + 32 * q] = raw[q];
-            const X* e = reinterpret_cast<const X*>(&raw[q]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float x = clean(e[i]);
-                if (x > best) { best = x; best_i = s0 + (v + 32 * q) * VEC + i - off; }
+    double sum0 = 0.0, sum1 = 0.0;
+    if (sum_now) {
+        W.at(best);
+        scan(v0 + lane, v1, 32, true, [&](const float (&x)[VEC], int i0, float hi) {
+            if (hi > best) {                                  // the sums so far, relative to the new maximum
+                W.at(hi);
+                const double f = W(best);
+                sum0 *= f;
+                sum1 *= f;
+                best = hi;
             }
-        }
+            add_mass<VEC>(W, x, i0, W.cutoff, any, sum0, sum1);
+        });
+    } else {
+        scan(v0 + lane, v1, 32, true, [&](const float (&)[VEC], int, float hi) { best = fmaxf(best, hi); });
     }
-    uint64_t top = block_reduce(rank_of(best, best_i), S.red64, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+    float mx = block_reduce(best, reinterpret_cast<float*>(S.red64), [](float x, float y) { return fmaxf(x, y); });
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    tell(S.x.best, top);
+    // Lower bounds of the row's k-th largest: the k-th largest of the threads' maxima, of whichever CTA has the highest;
+    // and, k / C of the candidates from each CTA, the lowest of their (k / C)-th.
+    float bound = -INFINITY, share = -INFINITY;
+    if (has_k && !alone && k <= NT) {
+        list[tid] = (uint64_t)order_key(best) << 32;
+        sort_falling(list, NT);
+        bound = key_value((uint32_t)(list[k - 1] >> 32));
+        share = key_value((uint32_t)(list[(k - 1) / C] >> 32));
+        tell(S.x.lo, (double)share);
+    }
+    tell(S.x.best, ((uint64_t)__float_as_uint(bound) << 32) | __float_as_uint(mx));
     meet();
-    for (int q = 0; q < C; ++q) top = max(top, S.x.best[q]);
-    const float mx = key_value((uint32_t)(top >> 32));
-    const int top_i = (int)(0xffffffffu - (uint32_t)top);
-    if (mx == -INFINITY || !(T > 0.f) || p <= 0.f) {          // nothing to choose from; greedy; the largest alone
+    for (int q = 0; q < C; ++q) {
+        mx = fmaxf(mx, __uint_as_float((uint32_t)S.x.best[q]));
+        bound = fmaxf(bound, __uint_as_float((uint32_t)(S.x.best[q] >> 32)));
+    }
+    if (has_k && !alone && k <= NT) {
+        for (int q = 0; q < C; ++q) share = fminf(share, (float)S.x.lo[q]);
+        bound = fmaxf(bound, share);
+    }
+    // f(x, index) for the entries >= thr (no NaN); threads and vectors without one are skipped
+    auto each_from = [&](float thr, auto f) {
+        if (!(best >= thr)) return;
+        each([&](const float (&x)[VEC], int i0, float hi) {
+            if (hi >= thr) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (x[i] >= thr) f(x[i], i0 + i);
+            }
+        });
+    };
+    auto mass_of = [&](float thr, auto pred) {                // this thread's share of the weights of the entries >= thr
+        double a = 0.0, b = 0.0;
+        thr = fmaxf(thr, W.cutoff);
+        if (best >= thr)
+            each([&](const float (&x)[VEC], int i0, float hi) { if (hi >= thr) add_mass<VEC>(W, x, i0, thr, pred, a, b); });
+        return a + b;
+    };
+    auto largest_alone = [&] {                                 // the lowest index of the maximum
+        int at = 0x7fffffff;
+        each_from(mx, [&](float, int i) { at = min(at, i); });
+        at = block_reduce(at, reinterpret_cast<int*>(S.red64), [](int a, int b) { return min(a, b); });
+        tell(S.x.cnt, (double)at);
+        meet();
         if (rank == 0 && tid == 0) {
-            P.tokens[r] = mx == -INFINITY ? -1 : top_i;
-            if (P.probs) P.probs[r] = mx == -INFINITY ? 0.f : 1.f;
+            double first = S.x.cnt[0];
+            for (int q = 1; q < C; ++q) first = fmin(first, S.x.cnt[q]);
+            P.tokens[r] = (int)first;
+            if (P.probs) P.probs[r] = 1.f;
+        }
+    };
+    if (mx == -INFINITY) {                                     // nothing to choose from
+        if (rank == 0 && tid == 0) {
+            P.tokens[r] = -1;
+            if (P.probs) P.probs[r] = 0.f;
         }
         return;
     }
-    Weights W;
-    W.set(mx, T, S.tab);
-    const double low = mp > 0.f ? (double)mp : 0.0;
-    const bool has_p = p < 1.f, has_k = k_in > 0 && k_in < P.V;
-    const int k = k_in;
-    uint64_t cut = 0;                                         // candidates below it are dropped
+    if (alone) {
+        largest_alone();
+        return;
+    }
+    double mine = 0.0;                                        // this thread's mass
+    if (mx == INFINITY) {
+        inf_max = true;
+        mx = 0.f;
+        best = best == INFINITY ? 0.f : -INFINITY;
+        bound = bound == INFINITY ? 0.f : -INFINITY;
+        W.at(mx);
+        if (sum_now) mine = mass_of(-FLT_MAX, any);
+    } else {
+        W.at(mx);
+        if (sum_now) mine = (sum0 + sum1) * W(best);
+    }
 
-    if (has_p || has_k) {
-        // ------------------------------------------------------------ the filters' boundary
-        float bound = -INFINITY;                              // elements below it cannot stay
-        double total = 0.0;
-        if (has_k) {
-            if (k <= kThreads) {
-                int g = 1;
-                while (g < 32 && kThreads / (2 * g) >= k) g *= 2;
-                float b = best;
-                for (int o = 1; o < g; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-                bound = key_value((uint32_t)block_reduce((uint64_t)order_key(b), S.red64, [](uint64_t x, uint64_t y) { return x < y ? x : y; }));
+    uint64_t cut = 0;                                         // candidates below it are dropped
+    bool pieces = false;                                      // S.wsum: the kept mass of each warp's piece
+    auto piece_sums = [&](double v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();
+        if (lane == 0) S.wsum[wid] = v;
+        __syncthreads();
+        double t = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += S.wsum[w];
+        return t;
+    };
+    // The chosen entries' ranks into the list of CTA 0; how many there are.
+    auto gather = [&](float thr, auto chosen) {
+        int n = 0;
+        each_from(thr, [&](float x, int i) {
+            if (!chosen(x)) return;
+            ++n;
+            const uint32_t at = C > 1 ? add_u32(&S.x.n_list, 0, 1u) : atomicAdd(&S.x.n_list, 1u);
+            if (at < (uint32_t)kList) {
+                if (C > 1) put(&list[at], 0, rank_of(x, i)); else list[at] = rank_of(x, i);
             }
-        } else {
-            bound = mx - T * (logf((float)P.V / (1.f - p)) + 0.01f);
-            double mine = 0.0;
-            each([&](float x, int) { mine += W(x); });
-            total = block_sum(mine, S.red);
-            tell(S.x.total, total);
+        });
+        tell(S.x.listed, (double)block_reduce(n, reinterpret_cast<int*>(S.red64), [](int a, int b) { return a + b; }));
+        meet();
+        return sum_of(S.x.listed);
+    };
+    auto sort_list = [&](int n) {
+        int m = 64;
+        while (m < n) m *= 2;
+        for (int i = n + tid; i < m; i += NT) list[i] = 0;
+        sort_falling(list, m);
+        return m;
+    };
+    // CTA 0 finishes the row from its list of n entries, the only ones that can stay; total: top-p's whole (without top-k).
+    auto finish = [&](int n, double total) {
+        const int m = sort_list(n), nk = has_k ? min(n, k) : n, per = (m + NT - 1) / NT;
+        double mine = 0.0, all;
+        for (int i = 0, q = tid * per; i < per && q < nk; ++i, ++q) mine += W(key_value((uint32_t)(list[q] >> 32)));
+        double cum = block_scan(mine, S.red, &all);
+        const double target = (double)p * (has_k ? all : total);
+        for (int i = 0, q = tid * per; i < per && q < m; ++i, ++q) {
+            const uint64_t e = list[q];
+            const double w = q < nk ? W(key_value((uint32_t)(e >> 32))) : 0.0;
+            const bool keep = q < nk && (q == 0 || ((!has_p || cum < target) && w >= low));
+            cum += w;
+            // next by rising index: complements fall
+            list[q] = keep ? ~(((uint64_t)(0xffffffffu - (uint32_t)e) << 32) | (uint32_t)(e >> 32)) : 0;
         }
-        // a histogram of the slice, then sums of the rank's share of the bins over the cluster
+        sort_falling(list, m);
+        mine = 0.0;
+        int last = -1;
+        for (int i = 0, q = tid * per; i < per && q < m; ++i, ++q) {
+            const uint64_t e = list[q];
+            const double w = e ? W(key_value((uint32_t)~e)) : 0.0;
+            if (w > 0.0) last = q;
+            mine += w;
+        }
+        cum = block_scan(mine, S.red, &all);
+        if (tid == 0) S.found = kList;
+        __syncthreads();
+        const double want = (double)u * all;
+        if (last >= 0 && cum + mine > want) {
+            for (int i = 0, q = tid * per; i < per && q < m; ++i, ++q) {
+                const double w = list[q] ? W(key_value((uint32_t)~list[q])) : 0.0;
+                cum += w;
+                if (w > 0.0 && cum > want) { atomicMin(&S.found, q); break; }
+            }
+        }
+        const int end = block_reduce(last, reinterpret_cast<int*>(S.red64), [](int a, int b) { return max(a, b); });
+        __syncthreads();
+        if (tid == 0) {
+            const uint64_t v = ~list[S.found < kList ? S.found : end];
+            P.tokens[r] = (int)(v >> 32);
+            if (P.probs) P.probs[r] = (float)(W(key_value((uint32_t)v)) / all);
+        }
+    };
+
+    bool bisect = false;
+    if (has_k) {
+        bisect = true;
+        if (bound > -INFINITY) {
+            const double n = gather(bound, [](float) { return true; });
+            if (n <= (double)kList) {
+                if (rank == 0) finish((int)n, 0.0);
+                return;
+            }
+        }
+    } else if (has_p) {
+        // ------------------------------------------------------------ the prefix's end
+        // At or below every x of bins 0 .. b.
+        auto edge_x = [&](int b) {
+            return b >= kBins - 1 ? -FLT_MAX : fmaxf(-FLT_MAX, mx - T * ((float)(b + 1) * (1.00002f / kPerUnit)) - 1e-6f * fabsf(mx));
+        };
+        bound = fmaxf(mx - T * (logf((float)P.V / (1.f - p)) + 0.01f), -FLT_MAX);
+        tell(S.x.total, block_sum(mine, S.red));
+        for (int i = tid; i < kBins; i += NT) hist[i] = place[i] = 0;
+        __syncthreads();
+        each_from(bound, [&](float x, int) {
+            const float z = W.z(x);
+            const int b = min((int)z, kBins - 1);
+            atomicAdd(&hist[b], 1u);
+            atomicAdd(&place[b], min((uint32_t)((z - (float)b) * 1024.f), 1023u));
+        });
+        meet();
+        const double total = sum_of(S.x.total), target = (double)p * total;
+        // sums of the rank's share of the bins over the cluster
         const int nb = kBins / C;
-        auto histogram = [&](auto bin_of) {                   // bin_of: -1 for an element that takes no part
-            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-            __syncthreads();
-            each([&](float x, int) {
-                const int b = bin_of(x);
-                if (b >= 0) atomicAdd(&hist[b], 1u);
-            });
-            meet();
+        auto lower = [&](int b, uint32_t n, float mean) {     // bounds of a bin's mass
+            return b == kBins - 1 ? 0.0 : (double)n * (1.0 - kSlack) * __expf(-((float)b + mean + 1.f / 1024.f) * (1.f / kPerUnit));
         };
-        // weight at the left edge of bin b: bins [z0, z0 + nz) of the first histogram over kBins
-        float z0 = 0.f, dz = 1.f;
-        auto edge = [&](int b) { return (double)__expf(-(z0 + dz * (float)b) * (1.f / kPerUnit)); };
-        auto lower = [&](int b) { return b == kBins - 1 ? 0.0 : edge(b + 1) * (1.0 - kSlack); };   // the last bin has no end
-        auto upper = [&](int b) { return edge(b) * (1.0 + kSlack); };
-        auto gather_bins = [&] {
-            double n = 0.0, lo = 0.0, up = 0.0;
-            for (int b = rank * nb + tid; b < (rank + 1) * nb; b += kThreads) {
-                uint32_t c = 0;
-                for (int q = 0; q < C; ++q) c += get_u32(&hist[b], q);
-                hist[b] = c;                                  // no other rank reads this rank's share before the next meeting
-                n += c;
-                if (!has_k) { lo += c * lower(b); up += c * upper(b); }
-            }
-            tell(S.x.cnt, block_sum(n, S.red));
-            if (!has_k) {
-                tell(S.x.lo, block_sum(lo, S.red));
-                tell(S.x.up, block_sum(up, S.red));
-            }
-            meet();
+        auto upper = [&](int b, uint32_t n, float mean) {     // (the last bin has no end)
+            return (double)n * (1.0 + kSlack) * 1.000031 * __expf(-((float)b + (b == kBins - 1 ? 0.f : mean)) * (1.f / kPerUnit));
         };
-        // The first bin at which the running sum of `slots` (a bin's count times weight(b)) reaches
-        // `want`, or the last; *before: elements of the bins before it, *upto: with its own.
-        auto cross = [&](const double* slots, auto weight, double want, double* before, double* upto) {
+        double n = 0.0, lo = 0.0, up = 0.0;
+        for (int b = rank * nb + tid; b < (rank + 1) * nb; b += NT) {
+            uint32_t c = 0;
+            double at = 0.0;
+            for (int q = 0; q < C; ++q) {
+                c += get_u32(&hist[b], q);
+                at += get_u32(&place[b], q);
+            }
+            const float mean = c > 0 ? (float)(at / (1024.0 * c)) : 0.f;
+            hist[b] = c;                                      // no other rank reads this rank's share before the next meeting
+            place[b] = __float_as_uint(mean);
+            n += c;
+            lo += lower(b, c, mean);
+            up += upper(b, c, mean);
+        }
+        n = block_sum(n, S.red);
+        lo = block_sum(lo, S.red);
+        up = block_sum(up, S.red);
+        tell(S.x.cnt, n);
+        tell(S.x.lo, lo);
+        tell(S.x.up, up);
+        meet();
+        // The first bin at which the running sum of `slots` (bins' measure) reaches the
+        // target, or the last of theirs; *before: elements of the bins before it, *upto: with its own.
+        auto cross = [&](const double* slots, auto measure, double* before, double* upto) {
             double sum = 0.0, cnt = 0.0;
             int q = 0;
-            for (; q < C - 1 && !(sum + slots[q] >= want); ++q) { sum += slots[q]; cnt += S.x.cnt[q]; }
-            const int per = (nb + kThreads - 1) / kThreads;
-            uint32_t c[kBins / kThreads];
-            double n = 0.0, v = 0.0;
+            for (; q < C - 1 && !(sum + slots[q] >= target); ++q) { sum += slots[q]; cnt += S.x.cnt[q]; }
+            const int per = (nb + NT - 1) / NT;
+            uint32_t c[kBins / NT];
+            double vi[kBins / NT], n = 0.0, v = 0.0;
 #pragma unroll
-            for (int i = 0; i < kBins / kThreads; ++i) {
+            for (int i = 0; i < kBins / NT; ++i) {
                 const int b = tid * per + i;
-                c[i] = i < per && b < nb ? get_u32(&hist[q * nb + b], q) : 0u;
+                const bool in = i < per && b < nb;
+                c[i] = in ? get_u32(&hist[q * nb + b], q) : 0u;
+                vi[i] = in ? measure(q * nb + b, c[i], __uint_as_float(get_u32(&place[q * nb + b], q))) : 0.0;
                 n += c[i];
-                v += c[i] * weight(q * nb + min(b, nb - 1));
+                v += vi[i];
             }
             double all_v, all_n;
             double pv = sum + block_scan(v, S.red, &all_v), pn = cnt + block_scan(n, S.red, &all_n);
-            if (tid == 0) { S.cross_bin = kBins; }
+            if (tid == 0) S.cross_bin = kBins;
             __syncthreads();
             int mine = kBins;
-            double mine_n = 0.0;
+            double mine_n = 0.0, mine_c = 0.0;
 #pragma unroll
-            for (int i = 0; i < kBins / kThreads; ++i) {
+            for (int i = 0; i < kBins / NT; ++i) {
                 const int b = tid * per + i;
                 if (i >= per || b >= nb) break;
-                pv += c[i] * weight(q * nb + b);
-                if (mine == kBins && pv >= want) { mine = q * nb + b; mine_n = pn; }
+                pv += vi[i];
+                if (mine == kBins && pv >= target) { mine = q * nb + b; mine_n = pn; mine_c = c[i]; }
                 pn += c[i];
             }
             if (mine < kBins) atomicMin(&S.cross_bin, mine);
             __syncthreads();
             const int bin = S.cross_bin;
-            if (mine == bin && mine < kBins) {
-                S.cross_before = mine_n;
-                S.found = (int)c[0];
-#pragma unroll
-                for (int i = 1; i < kBins / kThreads; ++i)
-                    if (tid * per + i == bin - q * nb) S.found = (int)c[i];
-            }
+            if (mine == bin && mine < kBins) { S.cross_before = mine_n; S.red[0] = mine_n + mine_c; }
             __syncthreads();
-            if (bin == kBins) {                               // not reached in these bins: their last
-                *before = cnt;
-                *upto = cnt + all_n;
-                return (q + 1) * nb - 1;
-            }
-            *before = S.cross_before;
-            *upto = S.cross_before + S.found;
-            return bin;
+            *before = bin < kBins ? S.cross_before : cnt;     // (not reached in these bins: their last)
+            *upto = bin < kBins ? S.red[0] : cnt + all_n;
+            __syncthreads();
+            return bin < kBins ? bin : (q + 1) * nb - 1;
         };
-        // The chosen elements' ranks into the list of CTA 0.
-        auto gather = [&](auto chosen) {
-            int n = 0;
-            each([&](float x, int) { n += chosen(x); });
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            uint32_t at = 0;
-            if (lane == 31 && inc > 0) at = add_u32(&S.x.n_list, 0, (uint32_t)inc);
-            at = __shfl_sync(0xffffffffu, at, 31) + (uint32_t)(inc - n);
-            if (n > 0)
-                each([&](float x, int i) {
-                    if (chosen(x) && at < (uint32_t)kList) put(&list[at++], 0, rank_of(x, i));
-                });
-            meet();
-        };
-        auto sort_list = [&](int n) {
-            int m = 64;
-            while (m < n) m *= 2;
-            for (int i = n + tid; i < m; i += kThreads) list[i] = 0;
-            sort_falling(list, m);
-            return m;
-        };
-        const double one = 1.0;
-        histogram([&](float x) { return x >= bound && x > -INFINITY ? W.bin(x) : -1; });
-        if (!has_k) total = sum_of(S.x.total);
-        gather_bins();
-        double before, upto;
-        const int b_hi = has_k ? cross(S.x.cnt, [&](int) { return one; }, (double)k, &before, &upto)
-                               : cross(S.x.lo, lower, (double)p * total, &before, &upto);
-        bool bisect = false;
+        double before, upto, skip;
+        const int b_lo = cross(S.x.lo, lower, &before, &upto);
         if (upto <= (double)kList) {
-            // -------------------------------------------------------- a short list: CTA 0 finishes the row
             meet();                                           // every rank has read the bins that the list overwrites
-            gather([&](float x) { return x >= bound && x > -INFINITY && W.bin(x) <= b_hi; });
-            if (rank != 0) return;
-            const int n = (int)min(S.x.n_list, (unsigned)kList), m = sort_list(n);
-            const int nk = has_k ? min(n, k) : n;
-            constexpr int PER = kList / kThreads;
-            uint64_t e[PER];
-            double w[PER], mine = 0.0, all;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int q = tid * PER + i;
-                e[i] = q < nk ? list[q] : 0;
-                w[i] = q < nk ? W(key_value((uint32_t)(e[i] >> 32))) : 0.0;
-                mine += w[i];
-            }
-            double cum = block_scan(mine, S.red, &all);
-            const double target = (double)p * (has_k ? all : total);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int q = tid * PER + i;
-                const bool keep = q < nk && (q == 0 || ((!has_p || cum < target) && w[i] >= low));
-                cum += w[i];
-                // by rising index: the largest key first after the complement
-                if (q < m) list[q] = keep ? ~(((uint64_t)(0xffffffffu - (uint32_t)e[i]) << 32) | (uint32_t)(e[i] >> 32)) : 0;
-            }
-            sort_falling(list, m);
-            mine = 0.0;
-            int last = -1;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int q = tid * PER + i;
-                e[i] = q < m ? list[q] : 0;
-                w[i] = e[i] ? W(key_value((uint32_t)~e[i])) : 0.0;
-                if (w[i] > 0.0) last = q;
-                mine += w[i];
-            }
-            cum = block_scan(mine, S.red, &all);
-            if (tid == 0) S.found = kList;
-            __syncthreads();
-            const double want = (double)u * all;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                cum += w[i];
-                if (w[i] > 0.0 && cum > want) { atomicMin(&S.found, tid * PER + i); break; }
-            }
-            const int end = (int)block_reduce((double)last, S.red, [](double a, double b) { return fmax(a, b); });
-            __syncthreads();
-            const int at = S.found < kList ? S.found : end;
-            if (tid == at / PER) {
-                const uint64_t v = ~list[at];
-                P.tokens[r] = (int)(v >> 32);
-                if (P.probs) P.probs[r] = (float)(W(key_value((uint32_t)v)) / all);
-            }
+            gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { return W.bin(x) <= b_lo; });
+            if (rank == 0) finish((int)upto, total);
             return;
         }
-        if (!has_k) {
-            // -------------------------------------------------------- a long prefix: the boundary's bins once more
-            const double target = (double)p * total;
-            double skip, skip2;
-            const int b_lo = b_hi, b_up = cross(S.x.up, upper, target, &skip, &skip2);
+        const int b_up = cross(S.x.up, upper, &before, &skip);
+        if (upto - before <= (double)kList) {
             meet();
-            z0 = (float)b_up;
-            dz = (float)(b_lo + 1 - b_up) / (float)kBins;
-            const float inv_dz = (float)kBins / (float)(b_lo + 1 - b_up);
-            auto sub = [&](float x) {                         // -1: above, kBins: below, else the finer bin
-                const int b = W.bin(x);
-                if (b < b_up) return -1;
-                if (b > b_lo || x == -INFINITY) return kBins;
-                return min((int)fminf((W.z(x) - z0) * inv_dz, 4096.f), kBins - 1);
-            };
-            double mine = 0.0;
-            histogram([&](float x) {
-                const int b = sub(x);
-                if (b < 0) mine += W(x);
-                return b < kBins ? b : -1;
-            });
-            const double above0 = block_sum(mine, S.red);
-            tell(S.x.above, above0);
-            meet();
-            const double above = sum_of(S.x.above);
-            gather_bins();
-            double n0, n1;
-            const int s_up = cross(S.x.up, upper, target - above, &n0, &skip);
-            const int s_lo = cross(S.x.lo, lower, target - above, &skip, &n1);
-            if (n1 - n0 <= (double)kList) {
-                meet();
-                double m2 = 0.0;
-                each([&](float x, int) {
-                    const int b = sub(x);
-                    if (b >= 0 && b < s_up) m2 += W(x);
-                });
-                tell(S.x.above2, block_sum(m2, S.red));
-                gather([&](float x) { const int b = sub(x); return b >= s_up && b <= s_lo; });
-                if (rank == 0) {
-                    const double a2 = above + sum_of(S.x.above2);
-                    const int n = (int)min(S.x.n_list, (unsigned)kList);
-                    sort_list(n);
-                    constexpr int PER = kList / kThreads;
-                    double w[PER], own = 0.0, all;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int q = tid * PER + i;
-                        w[i] = q < n ? W(key_value((uint32_t)(list[q] >> 32))) : 0.0;
-                        own += w[i];
-                    }
-                    double cum = a2 + block_scan(own, S.red, &all);
-                    int stay = 0;                             // the list's first `stay` entries stay
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        stay += tid * PER + i < n && cum < target;
-                        cum += w[i];
-                    }
-                    stay = (int)block_sum((double)stay, S.red);
-                    const uint64_t c = n == 0 ? 0 : stay > 0 ? list[stay - 1] : list[0] + 1;
-                    if (tid < C) put(&S.x.cut, tid, c);
+            // The mass above those bins (an x >= sure is in a bin above for sure: most need no bin); it stays,
+            // so without min_p it also is the start of the pieces' kept mass.
+            const float sure = mx - T * ((float)b_up * (0.99998f / kPerUnit)) + 1e-6f * fabsf(mx);
+            const double mass = b_up == 0 ? 0.0 : mass_of(edge_x(b_up - 1), [&](float x, int, double) { return x >= sure || W.bin(x) < b_up; });
+            tell(S.x.above, piece_sums(mass));
+            const int n = (int)gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { const int b = W.bin(x); return b >= b_up && b <= b_lo; });
+            if (rank == 0) {
+                const int per = (sort_list(n) + NT - 1) / NT;
+                double own = 0.0, all;
+                for (int i = 0, q = tid * per; i < per && q < n; ++i, ++q) own += W(key_value((uint32_t)(list[q] >> 32)));
+                double cum = sum_of(S.x.above) + block_scan(own, S.red, &all);
+                int stay = 0;                                 // the list's first `stay` entries stay
+                for (int i = 0, q = tid * per; i < per && q < n; ++i, ++q) {
+                    if (!(cum < target)) break;
+                    const double w = W(key_value((uint32_t)(list[q] >> 32)));
+                    ++stay;
+                    cum += w;
+                    const int j = (int)(0xffffffffu - (uint32_t)list[q]) + off, own_rank = j / P.slice;
+                    add_u64(&S.x.piece[(j - own_rank * P.slice) / VEC / per_warp], own_rank, (uint64_t)__double2ull_rn(w * kFixed));
                 }
-                meet();
-                cut = min(S.x.cut, top);                      // the largest always stays
-            } else {
-                bisect = true;
+                stay = block_reduce(stay, reinterpret_cast<int*>(S.red64), [](int a, int b) { return a + b; });
+                const uint64_t c = n == 0 ? 0 : stay > 0 ? list[stay - 1] : list[0] + 1;
+                if (tid < C) put(&S.x.cut, tid, c);
             }
+            meet();
+            cut = S.x.cut;
+            pieces = low == 0.0;
         } else {
             bisect = true;
         }
-        if (bisect) {
-            // -------------------------------------------------------- too many equal or too close: bisection of the rank
-            int turn = 0;
-            auto measure = [&](uint64_t c, bool with_c, bool mass, double* n) {   // of the candidates above c (and not below `cut`)
-                double nn = 0.0, mm = 0.0;
-                each([&](float x, int i) {
-                    const uint64_t v = rank_of(x, i);
-                    if (x > -INFINITY && v >= cut && (v > c || (with_c && v == c))) {
-                        nn += 1.0;
-                        if (mass) mm += W(x);
-                    }
-                });
-                nn = block_sum(nn, S.red);
-                if (mass) mm = block_sum(mm, S.red);
-                tell(S.x.bis_cnt[turn], nn);
-                tell(S.x.bis_mass[turn], mm);
-                meet();
-                *n = sum_of(S.x.bis_cnt[turn]);
-                const double t = sum_of(S.x.bis_mass[turn]);
-                turn ^= 1;
-                return t;
-            };
-            double n;
-            if (has_k) {                                      // the largest c with k candidates at or above it
-                measure(0, true, false, &n);
-                if (n > (double)k) {
-                    uint64_t lo = 0, hi = top + 1;
-                    while (hi - lo > 1) {
-                        const uint64_t mid = lo + ((hi - lo) >> 1);
-                        measure(mid, true, false, &n);
-                        if (n >= (double)k) lo = mid; else hi = mid;
-                    }
-                    cut = lo;
+    }
+    if (bisect) {
+        // ------------------------------------------------------------ too many equal or too close: bisection of the rank
+        int turn = 0;
+        const uint64_t top = rank_of(mx, 0);                  // no candidate comes before it
+        auto measure = [&](uint64_t c, bool with_c, bool mass, double* n) {   // of the candidates above c (and not below `cut`)
+            double nn = 0.0, mm = 0.0;
+            each_from(-FLT_MAX, [&](float x, int i) {
+                const uint64_t v = rank_of(x, i);
+                if (v >= cut && (v > c || (with_c && v == c))) {
+                    nn += 1.0;
+                    if (mass) mm += W(x);
                 }
-            }
-            if (has_p) {                                      // the smallest c with less than the target's mass above it
-                const double target = (double)p * measure(0, true, true, &n);
-                uint64_t lo = cut, hi = top;                  // hi always qualifies: nothing lies above it
-                while (lo < hi) {
+            });
+            nn = block_sum(nn, S.red);
+            if (mass) mm = block_sum(mm, S.red);
+            tell(S.x.bis_cnt[turn], nn);
+            tell(S.x.bis_mass[turn], mm);
+            meet();
+            *n = sum_of(S.x.bis_cnt[turn]);
+            const double t = sum_of(S.x.bis_mass[turn]);
+            turn ^= 1;
+            return t;
+        };
+        double n;
+        if (has_k) {                                          // the largest c with k candidates at or above it
+            measure(0, true, false, &n);
+            if (n > (double)k) {
+                uint64_t lo = 0, hi = top + 1;
+                while (hi - lo > 1) {
                     const uint64_t mid = lo + ((hi - lo) >> 1);
-                    if (measure(mid, false, true, &n) < target) hi = mid; else lo = mid + 1;
+                    measure(mid, true, false, &n);
+                    if (n >= (double)k) lo = mid; else hi = mid;
+                    if (n == (double)k) break;
                 }
                 cut = lo;
             }
+        }
+        if (has_p) {                                          // the smallest c with less than the target's mass above it
+            const double target = (double)p * measure(0, true, true, &n);
+            uint64_t lo = cut, hi = top;                      // hi always qualifies: nothing lies above it
+            while (lo < hi) {
+                const uint64_t mid = lo + ((hi - lo) >> 1);
+                if (measure(mid, false, true, &n) < target) hi = mid; else lo = mid + 1;
+            }
+            cut = lo;
         }
     }
 
     // -------------------------------------------------------------------- the draw, in the vocabulary's order
     const float cut_x = key_value((uint32_t)(cut >> 32));
     const uint32_t cut_i = 0xffffffffu - (uint32_t)cut;
-    auto weight = [&](float x, int i) {                       // 0: dropped
-        if (cut != 0 && !(x > cut_x || (x == cut_x && (uint32_t)i <= cut_i))) return 0.0;
-        const double w = W(x);
-        return w >= low || i == top_i ? w : 0.0;
-    };
-    double mine = 0.0;
-    each([&](float x, int i) { mine += weight(x, i); });
+    // (a little below where the weight falls to min_p: the weight itself decides)
+    const float thr = fmaxf(fmaxf(W.cutoff, cut != 0 ? cut_x : -FLT_MAX), low > 0.0 ? mx + 1.001f * T * logf(mp) - 1e-3f * T - 1e-6f * fabsf(mx) : -FLT_MAX);
+    auto kept = [&](float x, int i, double w) { return w >= low && !(cut != 0 && x == cut_x && (uint32_t)i > cut_i); };
+    double slice_sum;
+    if (pieces) {
+        if (tid < kWarps) S.wsum[tid] += (double)S.x.piece[tid] / kFixed;
+        __syncthreads();
+        slice_sum = 0.0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    __syncthreads();
-    if (lane == 0) S.wsum[wid] = mine;
-    __syncthreads();
-    double slice_sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) slice_sum += S.wsum[w];
+        for (int w = 0; w < kWarps; ++w) slice_sum += S.wsum[w];
+    } else {
+        slice_sum = piece_sums(sum_now && !has_p ? mine : mass_of(thr, kept));
+    }
     tell(S.x.kept, slice_sum);
     meet();
     const double all = sum_of(S.x.kept), want = (double)u * all;
@@ -633,6 +691,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(SampleParams P) {
         }
         cum += s;
     }
+    if (owner < 0) {                                          // (the filters always leave one)
+        largest_alone();
+        return;
+    }
     if (rank != owner) return;
     cum = owner_cum;
     int piece = -1;
@@ -646,56 +708,59 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(SampleParams P) {
         }
         cum += s;
     }
-    const int a0 = min(nvec, piece * per_warp), a1 = min(nvec, a0 + per_warp), each_n = (a1 - a0 + kThreads - 1) / kThreads;
+    const int a0 = min(nvec, piece * per_warp), a1 = min(nvec, a0 + per_warp), each_n = (a1 - a0 + NT - 1) / NT;
     const int t0 = min(a1, a0 + tid * each_n), t1 = min(a1, t0 + each_n);
+    auto piece_scan = [&](auto f) {
+        scan(t0, t1, 1, false, [&](const float (&x)[VEC], int i0, float hi) {
+            if (!(hi >= thr)) return;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const double w = x[i] >= thr ? W(x[i]) : 0.0;
+                if (w > 0.0 && kept(x[i], i0 + i, w)) f(w, i0 + i);
+            }
+        });
+    };
     mine = 0.0;
     int last = -1;
-    scan(t0, t1, 1, [&](float x, int i) {
-        const double w = weight(x, i);
-        if (w > 0.0) { mine += w; last = i; }
-    });
+    piece_scan([&](double w, int i) { mine += w; last = i; });
     double part;
     cum = piece_cum + block_scan(mine, S.red, &part);
     if (tid == 0) S.found = 0x7fffffff;
     __syncthreads();
     if (last >= 0 && cum + mine > want) {
         int hit = 0x7fffffff;
-        scan(t0, t1, 1, [&](float x, int i) {
-            const double w = weight(x, i);
-            if (w <= 0.0) return;
+        piece_scan([&](double w, int i) {
             cum += w;
             if (hit == 0x7fffffff && cum > want) hit = i;
         });
         atomicMin(&S.found, hit);
     }
-    const int end = (int)block_reduce((double)last, S.red, [](double a, double b) { return fmax(a, b); });
+    const int end = block_reduce(last, reinterpret_cast<int*>(S.red64), [](int a, int b) { return max(a, b); });
     __syncthreads();
     if (tid == 0) {
         const int at = S.found != 0x7fffffff ? S.found : end;
         P.tokens[r] = at;
-        if (P.probs) P.probs[r] = (float)(W(clean(row[at])) / all);
+        if (P.probs) P.probs[r] = (float)(W(value(row[at])) / all);
     }
 }
-
-constexpr size_t kSliceBytes = 65536;                // three CTAs an SM
-constexpr size_t kSliceMax = 196608;
 
 template <typename X>
 cudaError_t launch(SampleParams P, cudaStream_t s) {
     constexpr int VEC = 16 / (int)sizeof(X);
-    // The row is split until a slice fits a third of an SM's shared memory, and further while the
-    // rows alone leave SMs idle and a slice is long enough to pay for the exchanges.
     auto slice = [&](int c) { return (int)(((int64_t)P.V + VEC - 1 + c - 1) / c + VEC - 1) / VEC * VEC; };
+    // Rows are split while they leave SMs idle (148, two CTAs each) and a slice is long enough to pay for the exchanges.
     int c = 1;
-    while (c < kMaxCluster && (slice(c) * sizeof(X) > kSliceBytes + 64 || ((int64_t)P.rows * c < 444 && slice(c) > 8192))) c *= 2;
+    while (c < kMaxCluster && (int64_t)P.rows * c * 2 <= 320 && slice(c) > 4096) c *= 2;
     P.cluster = c;
     P.slice = slice(c);
-    P.resident = P.slice * sizeof(X) <= kSliceMax;
+    // Shared memory for two CTAs an SM, or for one where there are no more CTAs than SMs.
+    const size_t room = ((int64_t)P.rows * c <= 148 ? 208 * 1024 : 104 * 1024) - kHeadBytes;
+    P.resident = P.slice * sizeof(X) <= room;
     const size_t smem = kHeadBytes + (P.resident ? P.slice * sizeof(X) : 0);
     auto kern = sample_kernel<X>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kHeadBytes + kSliceMax));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 208 * 1024);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) e = launch_pdl_cluster(kern, dim3((unsigned)(P.rows * c)), dim3(kThreads), c, smem, s, P);
+    if (e == cudaSuccess) e = launch_pdl_cluster(kern, dim3((unsigned)(P.rows * c)), dim3(NT), c, smem, s, P);
     return e;
 }
 
