@@ -26,7 +26,7 @@
 // start and the units that a cut crosses. Those units' pieces write O / l (fp32) and (m, l)
 // per row, which a merge kernel joins in order: results do not depend on timing.
 //
-// Warp roles: NQ * 4 softmax warps (thread = query row = TMEM lane), then one warp
+// Warp roles: 8 softmax warps (TMEM lane = query row; NQ = 1: two threads to a row), then one warp
 // each for the loads, the MMAs, and zeroing V rows outside the unit's keys (those
 // rows may hold anything; P = 0 times NaN would poison O. K needs no care:
 // masked scores are replaced). Every wait is bounded.
@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "paged.h"
 #include "tc_ptx.cuh"
@@ -57,7 +58,7 @@ struct MergeUnit { int b, g, qt, c0, odd, c1; };         // pieces: slot 2 c0 + 
 struct Params {
     PagedAttn a;
     Share* shares; MergeUnit* merges;
-    float* part_o; float* part_ml;   // [2 kGrid][NQ * 128][hd], [..][2]
+    float4* part_o; float2* part_ml;  // [2 kGrid][NQ][hd / 4][128], [2 kGrid][NQ][128]
     int tpt, tpu;                    // tokens per query tile, per unit
     int page_shift;
     int32_t* status;
@@ -260,6 +261,53 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 lanes in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_out(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// 2^x for two x in [-126, 127) on the FMA pipe: the nearest integer goes into the exponent, 2^f on |f| <= 1/2 is a polynomial
+// of degree 5 fitted for the relative error (within 2^-23.6). The special function unit does 16
+// a clock, which is what a 128 x 128 tile's two products leave time for: a quarter of them here makes room.
+__device__ __forceinline__ void exp2_poly(uint64_t x, float& p0, float& p1) {
+    const uint64_t magic = f2(12582912.f, 12582912.f);          // 1.5 2^23: the sum's low bits are the integer
+    const uint64_t t = add2(x, magic), n = add2(t, f2(-12582912.f, -12582912.f)), f = fma2(n, f2(-1.f, -1.f), x);
+    uint64_t p = fma2(f2(1.327647129073739e-3f, 1.327647129073739e-3f), f, f2(9.675540961325169e-3f, 9.675540961325169e-3f));
+    p = fma2(p, f, f2(5.550713092088699e-2f, 5.550713092088699e-2f));
+    p = fma2(p, f, f2(0.24022120237350464f, 0.24022120237350464f));
+    p = fma2(p, f, f2(0.6931469440460205f, 0.6931469440460205f));
+    p = fma2(p, f, f2(1.0000001192092896f, 1.0000001192092896f));
+    float a, b, ta, tb;
+    f2_out(p, a, b);
+    f2_out(t, ta, tb);
+    p0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23));
+    p1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// A value that all lanes share, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -284,14 +332,20 @@ struct Cfg {
     static constexpr int kChunk = kRows * 128;                // a chunk of a query tile
     static constexpr int kTile = KT * HD * 2;                 // a K or V tile
     static constexpr int kQBytes = QTMEM ? 0 : NQ * NCH * kChunk;
-    static constexpr int kSlotsFit = (int)((kSmemMax - 1024 - 512 - kQBytes) / kTile);
+    // Softmax threads per query row. With one query tile its softmax is the chain that the MMAs wait for, so
+    // two threads share a row; with two tiles one's softmax runs beside the other's MMAs, and two
+    // threads would not have the registers.
+    static constexpr int SP = NQ == 1 ? 2 : 1;
+    static constexpr int kSoft = NQ * SP * 128;
+    static constexpr int kThreads = kSoft + 96;
+    static constexpr int CH = KT / SP;                        // a thread's keys of a tile
+    static constexpr int kTail = 512 + (SP == 2 ? kSoft * 8 : 0);   // barriers; two numbers per softmax thread
+    static constexpr int kSlotsFit = (int)((kSmemMax - 1024 - kTail - kQBytes) / kTile);
     static constexpr int NS = kSlotsFit < 12 ? kSlotsFit : 12;
     static constexpr int kQPerSlot = kTile / kChunk;          // staged query chunks per slot
     static constexpr int kQSlots = QTMEM ? (NCH + kQPerSlot - 1) / kQPerSlot : 0;
-    static constexpr int kSoft = NQ * 128;                    // softmax threads
-    static constexpr int kThreads = kSoft + 96;
     static constexpr int kOCol = 2 * KT, kQCol = 2 * KT + HD; // TMEM columns: S buffers, O tiles, Q
-    static constexpr size_t kSmem = 1024 + kQBytes + (size_t)NS * kTile + 512;
+    static constexpr size_t kSmem = 1024 + kQBytes + (size_t)NS * kTile + kTail;
     static_assert(kSmem <= kSmemMax, "shared memory");
     static_assert(2 * KT + NQ * HD + (QTMEM ? HD / 2 : 0) <= 512, "tensor memory");
 };
@@ -303,7 +357,8 @@ struct Bars {
     uint32_t tmem;
     int abort;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+constexpr int kBarBytes = 512;
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 // Ring entries before tile t's K and V within a piece of nt tiles: the order the MMAs take them in.
 template <int NQ> __device__ __forceinline__ int k_entry(int t) { return NQ == 2 ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
@@ -321,14 +376,15 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     uint8_t* sQ = base;                                       // [NQ][NCH][128 rows x 128 B]
     uint8_t* ring = base + C::kQBytes;                        // NS tiles, [NCH][KT rows x 128 B]
     Bars& B = *reinterpret_cast<Bars*>(ring + (size_t)NS * C::kTile);
+    float* s_half = reinterpret_cast<float*>(ring + (size_t)NS * C::kTile + kBarBytes);   // [2][SP][128]
     volatile int* abort_flag = &B.abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kLoadWarp = NQ * 4, kMmaWarp = NQ * 4 + 1, kFixWarp = NQ * 4 + 2;
+    constexpr int kLoadWarp = C::kSoft / 32, kMmaWarp = kLoadWarp + 1, kFixWarp = kLoadWarp + 2;
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) { mbar_init(&B.full[i], 1); mbar_init(&B.free_[i], 1); mbar_init(&B.vissued[i], 1); mbar_init(&B.vready[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&B.sdone[i], 1); mbar_init(&B.pready[i], 128); mbar_init(&B.odone[i], 1); }
-        mbar_init(&B.qfull, C::QTMEM ? 128 : 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&B.sdone[i], 1); mbar_init(&B.pready[i], C::SP * 128); mbar_init(&B.odone[i], 1); }
+        mbar_init(&B.qfull, C::QTMEM ? C::SP * 128 : 1);
         mbar_init(&B.qfree, 1);
         mbar_init(&B.spare, 1);
         B.abort = 0;
@@ -408,8 +464,8 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 __syncwarp();
                 if (page != -2) {
                     const int key = k0 + sub * box;
-                    tma_load_4d(ring + (size_t)s * C::kTile + ch * (KT * 128) + sub * (box * 128), m, &B.full[s], ch * 64, p.g,
-                                key & (P.a.page_size - 1), page);
+                    tma_load_2d(ring + (size_t)s * C::kTile + ch * (KT * 128) + sub * (box * 128), m, &B.full[s], p.g * HD + ch * 64,
+                                page * P.a.page_size + (key & (P.a.page_size - 1)));
                 }
                 ++e;
                 issued = e;
@@ -434,27 +490,34 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             if (!C::QTMEM && in && p.index >= 0) mbar_wait_until(&B.qfull, (uint32_t)p.index & 1u, global_timer_ns() + 1000000ull);
         }
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMAs (one thread)
-        if (lane == 0) {
-            uint32_t vpar = 0;                                // parity of each slot's next vready phase
-            constexpr uint32_t id_qk = idesc<T>(kRows, KT, 0), id_pv = idesc<T>(kRows, HD, 1);
-            while (ok && walk.next(P, &p)) {
-                if (p.nt == 0) continue;
-                const int e0 = e + C::kQSlots, ns = p.nt * NQ;
-                if (!mbar_wait(&B.qfull, (uint32_t)p.index & 1u, abort_flag, P.status)) { ok = false; break; }
+        // ------------------------------------------------------------ MMAs
+        // The whole warp runs the loop, so that what an MMA takes (descriptors, addresses) stays in uniform
+        // registers; one elected thread issues.
+        uint32_t vpar = 0;                                    // parity of each slot's next vready phase
+        constexpr uint32_t id_qk = idesc<T>(kRows, KT, 0), id_pv = idesc<T>(kRows, HD, 1);
+        const bool leader = elect_one();
+        const uint32_t ring0 = smem_u32(ring), q0 = smem_u32(sQ);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, P.status); };
+        while (ok && walk.next(P, &p)) {
+            if (p.nt == 0) continue;
+            const int e0 = uniform(e) + C::kQSlots, nt = uniform(p.nt), ns = nt * NQ, k_first = uniform(p.t0) * KT, lo = uniform(p.lo), hi = uniform(p.hi);
+            const int g0 = uniform(gs);
+            if (!__all_sync(0xffffffffu, wait(&B.qfull, (uint32_t)p.index & 1u))) { ok = false; break; }
+            if (leader)
                 for (int s = 0; s < C::kQSlots; ++s) mbar_arrive(&B.free_[(e + s) % NS]);
-                auto issue_s = [&](int s) {
-                    const int t = s / NQ, q = s % NQ, en = e0 + k_entry<NQ>(t), sl = en % NS, buf = (gs + s) & 1;
-                    if (q == 0 && !mbar_wait(&B.full[sl], (uint32_t)(en / NS) & 1u, abort_flag, P.status)) return false;
-                    tc_fence_after();
+            auto issue_s = [&](int s) {
+                const int t = s / NQ, q = s % NQ, en = e0 + k_entry<NQ>(t), sl = en % NS, buf = (g0 + s) & 1;
+                if (q == 0 && !__all_sync(0xffffffffu, wait(&B.full[sl], (uint32_t)(en / NS) & 1u))) return false;
+                tc_fence_after();
+                if (leader) {
                     const uint32_t d = tmem + (uint32_t)(buf * KT);
-                    const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)sl * C::kTile));
+                    const uint64_t bd = sdesc_k_sw128(ring0 + (uint32_t)sl * C::kTile);
                     if (C::QTMEM) {
 #pragma unroll
                         for (int j = 0; j < HD / 16; ++j)
                             mma_f16_ts(d, tmem + (uint32_t)(C::kQCol + 8 * j), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
                     } else {
-                        const uint64_t ad = sdesc_k_sw128(smem_u32(sQ + q * NCH * C::kChunk));
+                        const uint64_t ad = sdesc_k_sw128(q0 + (uint32_t)(q * NCH * C::kChunk));
 #pragma unroll
                         for (int j = 0; j < HD / 16; ++j)
                             mma_bf16(d, ad + (uint64_t)(((j >> 2) * C::kChunk + (j & 3) * 32) >> 4), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
@@ -462,37 +525,41 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     mma_commit(&B.sdone[buf]);
                     if (q == NQ - 1) mma_commit(&B.free_[sl]);
                     if (!C::QTMEM && s == ns - 1) mma_commit(&B.qfree);
-                    return true;
-                };
-                if (!issue_s(0) || (ns > 1 && !issue_s(1))) { ok = false; break; }
-                for (int s = 0; s < ns; ++s) {
-                    const int t = s / NQ, q = s % NQ, en = e0 + v_entry<NQ>(t, p.nt), sl = en % NS, buf = (gs + s) & 1;
-                    if (q == 0) {
-                        const int k0 = (p.t0 + t) * KT;
-                        if (k0 < p.lo || k0 + KT > p.hi) {    // rows outside the unit's keys: zeroed first
-                            if (!mbar_wait(&B.vready[sl], (vpar >> sl) & 1u, abort_flag, P.status)) { ok = false; break; }
-                            vpar ^= 1u << sl;
-                        } else if (!mbar_wait(&B.full[sl], (uint32_t)(en / NS) & 1u, abort_flag, P.status)) { ok = false; break; }
-                    }
-                    if (!mbar_wait(&B.pready[buf], (uint32_t)((gs + s) >> 1) & 1u, abort_flag, P.status)) { ok = false; break; }
-                    tc_fence_after();
+                }
+                return true;
+            };
+            if (!issue_s(0) || (ns > 1 && !issue_s(1))) { ok = false; break; }
+            for (int s = 0; s < ns; ++s) {
+                const int t = s / NQ, q = s % NQ, en = e0 + v_entry<NQ>(t, nt), sl = en % NS, buf = (g0 + s) & 1;
+                if (q == 0) {
+                    const int k0 = k_first + t * KT;
+                    const bool part = k0 < lo || k0 + KT > hi;    // rows outside the unit's keys: zeroed first
+                    uint64_t* bar = part ? &B.vready[sl] : &B.full[sl];
+                    const uint32_t par = part ? (vpar >> sl) & 1u : (uint32_t)(en / NS) & 1u;
+                    if (!__all_sync(0xffffffffu, wait(bar, par))) { ok = false; break; }
+                    if (part) vpar ^= 1u << sl;
+                }
+                if (!__all_sync(0xffffffffu, wait(&B.pready[buf], (uint32_t)((g0 + s) >> 1) & 1u))) { ok = false; break; }
+                tc_fence_after();
+                if (leader) {
                     const uint32_t d = tmem + (uint32_t)(C::kOCol + q * HD), pa = tmem + (uint32_t)(buf * KT);
-                    const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)sl * C::kTile), KT * 128);
+                    const uint64_t bd = sdesc_mn_sw128(ring0 + (uint32_t)sl * C::kTile, KT * 128);
 #pragma unroll
                     for (int j = 0; j < KT / 16; ++j)
-                        mma_f16_ts(d, pa + (uint32_t)(8 * j), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
+                        mma_f16_ts(d, pa + (uint32_t)(j / (C::CH / 16) * C::CH + j % (C::CH / 16) * 8), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
                     mma_commit(&B.odone[buf]);
                     if (q == NQ - 1) mma_commit(&B.free_[sl]);
-                    if (s + 2 < ns && !issue_s(s + 2)) { ok = false; break; }
                 }
-                e = e0 + 2 * p.nt;
-                gs += ns;
+                if (s + 2 < ns && !issue_s(s + 2)) { ok = false; break; }
             }
-            if (!ok) {                                        // MMAs in flight end first (bounded)
-                mma_commit(&B.spare);
-                if (!mbar_wait_until(&B.spare, 0u, global_timer_ns() + kWaitLimitNs)) atomicOr(P.status, DSPARK_DEV_WAIT_TIMEOUT);
-            }
+            e = e0 + 2 * nt;
+            gs = g0 + ns;
         }
+        if (!ok && leader) {                                  // MMAs in flight end first (bounded)
+            mma_commit(&B.spare);
+            if (!mbar_wait_until(&B.spare, 0u, global_timer_ns() + kWaitLimitNs)) atomicOr(P.status, DSPARK_DEV_WAIT_TIMEOUT);
+        }
+        __syncwarp();
     } else if (warp == kFixWarp) {
         // ------------------------------------------------------------ V rows outside the unit's keys
         // (this warp skips entries, so a slot's load is first known to be issued: only then does the
@@ -521,15 +588,21 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             }
             e = e0 + 2 * p.nt;
         }
-    } else {
-        // ------------------------------------------------------------ softmax: one thread per query row
-        const int q = NQ == 2 ? tid >> 7 : 0, r = tid & 127;
+    } else if (warp < kLoadWarp) {
+        // ------------------------------------------------------------ softmax: SP threads per query row
+        // SP = 2: threads r and r + 128 share row r, each takes half of the tile's keys and half of
+        // the output's columns; they agree on the maximum through shared memory.
+        constexpr int SP = C::SP, CH = C::CH, OH = HD / SP;
+        const int q = SP == 2 ? 0 : tid >> 7, half = SP == 2 ? tid >> 7 : 0, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tO = tmem + (uint32_t)(C::kOCol + q * HD) + lane_off;
+        const uint32_t tO = tmem + (uint32_t)(C::kOCol + q * HD + half * OH) + lane_off;
         const float c = P.a.scale * 1.4426950408889634f;      // scores to log2
+        float* mine = s_half + half * 128 + r;
+        const float* other = s_half + (half ^ 1) * 128 + r;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
         };
+        auto agree = [&](bool good) { return SP == 1 ? good : !named_barrier_or(1, 256, !good); };   // a row's threads meet; false if one gave up
         const int grp = P.a.grp, tok_r = r / grp, head_r = r - tok_r * grp;
         while (ok && walk.next(P, &p)) {
             const int i = p.qt * P.tpu + q * P.tpt + tok_r;   // this row's token of the request
@@ -541,68 +614,84 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             const int i_first = p.qt * P.tpu + q * P.tpt, i_last = min(p.r.n, i_first + P.tpt) - 1;
             const int all_hi = P.a.causal ? min(p.r.L, p.r.L - p.r.n + i_first + 1) : p.r.L;
             const int all_lo = P.a.window > 0 ? max(0, p.r.L - p.r.n + i_last - P.a.window + 1) : 0;
+            const bool live = __any_sync(0xffffffffu, valid);  // the warp has a row to compute (the MMAs read garbage for the others)
             float m = -INFINITY, l = 0.f;
             if (C::QTMEM && p.nt > 0) {
                 // the staged query rows into tensor memory, two 16-bit values per column; the S products of
                 // the piece before have all completed (their last was waited for)
-                const bool live = r < P.tpt * grp;
+                const bool filled = r < P.tpt * grp;
                 for (int s = 0; s < C::kQSlots && ok; ++s) {
                     const int en = e + s, sl = en % NS;
                     if (!wait(&B.full[sl], (uint32_t)(en / NS) & 1u)) { ok = false; break; }
                     const int c0 = s * C::kQPerSlot, c1 = min(NCH, c0 + C::kQPerSlot);
                     for (int cc = c0; cc < c1; ++cc) {
                         const uint8_t* line = ring + (size_t)sl * C::kTile + (cc - c0) * C::kChunk + r * 128;
+                        static_assert(!C::QTMEM || SP == 2, "each thread of a row stages half a line");
+                        const int j0 = 4 * half;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int j0 = 0; j0 < 8; j0 += 4) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                                if (live) u = *reinterpret_cast<const uint4*>(line + (((j0 + j) ^ (r & 7)) * 16));
-                                w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
-                            }
-                            tmem_st_x16(tmem + (uint32_t)(C::kQCol + cc * 32 + j0 * 4) + lane_off, w);
+                        for (int j = 0; j < 4; ++j) {
+                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                            if (filled) u = *reinterpret_cast<const uint4*>(line + (((j0 + j) ^ (r & 7)) * 16));
+                            w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
                         }
+                        tmem_st_x16(tmem + (uint32_t)(C::kQCol + cc * 32 + j0 * 4) + lane_off, w);
                     }
                 }
-                if (!ok) break;
-                tmem_st_wait();
-                fence_async_shared();                         // reads done before the slots are loaded again
-                tc_fence_before();
-                mbar_arrive(&B.qfull);                        // the MMA thread then frees the slots
+                if (ok) {
+                    tmem_st_wait();
+                    fence_async_shared();                     // reads done before the slots are loaded again
+                    tc_fence_before();
+                    mbar_arrive(&B.qfull);                    // the MMA thread then frees the slots
+                }
             }
+            bool good = ok;
             int last_step = -1;
             for (int t = 0; t < p.nt; ++t) {
                 const int st = gs + t * NQ + q, buf = st & 1;
-                const uint32_t tS = tmem + (uint32_t)(buf * KT) + lane_off;
-                if (!wait(&B.sdone[buf], (uint32_t)(st >> 1) & 1u)) { ok = false; break; }
+                const uint32_t tS = tmem + (uint32_t)(buf * KT + half * CH) + lane_off;
+                good = good && wait(&B.sdone[buf], (uint32_t)(st >> 1) & 1u);
                 tc_fence_after();
-                uint32_t u[KT];
-#pragma unroll
-                for (int j = 0; j < KT; j += 32) tmem_ld_x32(tS + (uint32_t)j, u + j);
-                tmem_ld_wait();
                 const int k0 = (p.t0 + t) * KT;
-                if (k0 < all_lo || k0 + KT > all_hi) {        // some row does not see some key
-                    const int a = row_lo - k0, b = row_hi - k0;
+                const bool edge = k0 < all_lo || k0 + KT > all_hi;   // some row does not see some key
+                // At most 64 columns of scores at a time: 128 (SP = 1) are read once for the maximum and again
+                // for the exponentials, as they would not stay in registers.
+                constexpr int W = CH < 64 ? CH : 64;
+                uint32_t u[W];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto fetch = [&](int j) {                     // columns j .. j + W of this half
 #pragma unroll
-                    for (int j = 0; j < KT; ++j)
-                        if (j < a || j >= b) u[j] = 0xff800000u;
+                    for (int i = 0; i < W; i += 32) tmem_ld_x32(tS + (uint32_t)(j + i), u + i);
+                    tmem_ld_wait();
+                    if (edge) {
+                        const int a = row_lo - k0 - half * CH - j, b = row_hi - k0 - half * CH - j;
+#pragma unroll
+                        for (int i = 0; i < W; ++i)
+                            if (i < a || i >= b) u[i] = 0xff800000u;
+                    }
+                };
+#pragma unroll
+                for (int j = CH - W; j >= 0 && live; j -= W) {
+                    fetch(j);
+#pragma unroll
+                    for (int i = 0; i < W; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
                 }
-                float mx[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(u[j]);
-#pragma unroll
-                for (int j = 4; j < KT; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(u[j]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (SP == 2) mine[(t & 1) * 256] = top;       // two sets in turn: the other thread may still read the last
+                if (!agree(good)) { ok = false; break; }
+                if (SP == 2) top = fmaxf(top, other[(t & 1) * 256]);
+                top *= c;
                 const bool need = m > -INFINITY && top > m + kRescale;
-                if (__any_sync(0xffffffffu, need)) {
+                if (__any_sync(0xffffffffu, need && live)) {
                     // O holds the tiles before at the old maximum: their PV must have landed
-                    if (!wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u)) { ok = false; break; }
+                    good = wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u);
                     tc_fence_after();
                     const float f = need ? ex2(m - top) : 1.f;
                     if (need) { l *= f; m = top; }
-#pragma unroll
-                    for (int d = 0; d < HD; d += 16) {
+#pragma unroll 1
+                    for (int d = 0; d < OH; d += 16) {
                         uint32_t o[16];
                         tmem_ld_x16(tO + (uint32_t)d, o);
                         tmem_ld_wait();
@@ -614,35 +703,60 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 }
                 if (m == -INFINITY) m = top;                  // nothing summed yet
                 const float neg = m == -INFINITY ? 0.f : -m;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = f2(c, c), neg2 = f2(neg, neg);
+                uint64_t ls[2] = {0, 0};
+                // poly: a quarter of the exponentials on the FMA pipe (scores of -infinity have no place there)
+                auto exps = [&](int j0, auto poly) {
 #pragma unroll
-                for (int j = 0; j < KT; j += 32) {
-                    uint32_t w[16];
+                    for (int j = 0; j < W; j += 16) {
+                        uint32_t w[8];
 #pragma unroll
-                    for (int jj = 0; jj < 32; jj += 2) {
-                        const float p0 = ex2(fmaf(__uint_as_float(u[j + jj]), c, neg)), p1 = ex2(fmaf(__uint_as_float(u[j + jj + 1]), c, neg));
-                        ls[(jj >> 1) & 3] += p0 + p1;
-                        w[jj >> 1] = pack2<T>(p0, p1);
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint64_t x = fma2(f2(__uint_as_float(u[j + i]), __uint_as_float(u[j + i + 1])), c2, neg2);
+                            float p0, p1, x0, x1;
+                            f2_out(x, x0, x1);
+                            if (poly.value && (i & 6) == 6) {
+                                exp2_poly(f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f)), p0, p1);
+                            } else {
+                                p0 = ex2(x0);
+                                p1 = ex2(x1);
+                            }
+                            ls[(i >> 1) & 1] = add2(ls[(i >> 1) & 1], f2(p0, p1));
+                            w[i >> 1] = pack2<T>(p0, p1);
+                        }
+                        tmem_st_x8(tS + (uint32_t)((j0 + j) / 2), w);       // (over scores already used)
                     }
-                    tmem_st_x16(tS + (uint32_t)(j / 2), w);
+                };
+#pragma unroll
+                for (int j = 0; j < CH && live; j += W) {
+                    if (j > 0) fetch(j);
+                    if (edge) exps(j, std::false_type{}); else exps(j, std::true_type{});
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                float l0, l1;
+                f2_out(add2(ls[0], ls[1]), l0, l1);
+                l += l0 + l1;
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&B.pready[buf]);
                 last_step = st;
             }
-            if (!ok) break;
             // ---- the piece's result
-            if (p.nt > 0 && !wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u)) { ok = false; break; }
+            if (!ok) break;                                   // (all of the tile's warps)
+            if (p.nt > 0) good = good && wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u);
             tc_fence_after();
+            if (SP == 2) mine[(p.nt & 1) * 256] = l;
+            if (!agree(good)) { ok = false; break; }
+            if (SP == 2) {
+                l += other[(p.nt & 1) * 256];
+                named_barrier_sync(1, 256);                   // both have read: the next piece may write
+            }
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t tok = p.r.t0 + i;
             const int h = p.g * grp + head_r;
             if (p.whole) {
-                T* out = static_cast<T*>(P.a.out) + tok * P.a.out_stride + (int64_t)h * HD;
+                T* out = static_cast<T*>(P.a.out) + tok * P.a.out_stride + (int64_t)h * HD + half * OH;
 #pragma unroll
-                for (int d = 0; d < HD; d += 32) {
+                for (int d = 0; d < OH; d += 32) {
                     uint32_t o[32];
                     if (p.nt > 0) {
                         tmem_ld_x32(tO + (uint32_t)d, o);
@@ -659,19 +773,21 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                         }
                     }
                 }
-                if (valid && P.a.lse) P.a.lse[tok * P.a.nH + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                if (valid && half == 0 && P.a.lse) P.a.lse[tok * P.a.nH + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
             } else {
-                const int64_t row = (int64_t)p.slot * (NQ * kRows) + q * kRows + r;
-                if (valid) *reinterpret_cast<float2*>(P.part_ml + row * 2) = make_float2(l > 0.f ? m : -INFINITY, l);
+                // [slot][column / 4][row] float4: a warp's rows are neighbours
+                const int64_t part = (int64_t)p.slot * NQ + q;
+                if (valid && half == 0) P.part_ml[part * kRows + r] = make_float2(l > 0.f ? m : -INFINITY, l);
+                float4* po = P.part_o + (part * (HD / 4) + half * (OH / 4)) * kRows + r;
 #pragma unroll
-                for (int d = 0; d < HD; d += 32) {
+                for (int d = 0; d < OH; d += 32) {
                     uint32_t o[32];
                     tmem_ld_x32(tO + (uint32_t)d, o);
                     tmem_ld_wait();
                     if (valid) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4*>(P.part_o + row * HD + d + j) =
+                            po[(d + j) / 4 * kRows] =
                                 make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv, __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
                     }
                 }
@@ -690,49 +806,59 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 }
 
 // ------------------------------------------------------------------ merge
-// out = sum_s w_s O_s / sum_s w_s, w_s = l_s exp2(m_s - M), over a unit's pieces in order: one warp per row.
-constexpr int kMergeWarps = 8;
+// out = sum_s w_s O_s / sum_s w_s, w_s = l_s exp2(m_s - M), over a unit's pieces in order. A thread has four columns
+// of a row, neighbouring threads neighbouring rows (as the pieces lie): grid (units, row groups, column groups).
+constexpr int kMergeCols = 8;                                 // float4 columns per block
 template <typename T, int HD, int NQ>
-__global__ void __launch_bounds__(kMergeWarps * 32) attend_paged_merge_kernel(Params P) {
-    constexpr int PER = HD / 32;
+__global__ void __launch_bounds__(32 * kMergeCols) attend_paged_merge_kernel(Params P) {
     pdl_trigger();
     pdl_wait();
     const MergeUnit u = P.merges[blockIdx.x];
     if (u.c1 < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = blockIdx.y * kMergeWarps + warp, q = rr / kRows, r = rr % kRows;
+    const int q = blockIdx.y / (kRows / 32), r = (blockIdx.y % (kRows / 32)) * 32 + (threadIdx.x & 31);
+    const int col = blockIdx.z * kMergeCols + (threadIdx.x >> 5);
     const Req req = load_req(P.a, u.b);
     const int tr = r / P.a.grp, i = u.qt * P.tpu + q * P.tpt + tr;
     if (tr >= P.tpt || i >= req.n) return;
     const int h = u.g * P.a.grp + r - tr * P.a.grp, n = u.c1 - u.c0 + 1;
-    auto row_of = [&](int s) { return (int64_t)(s == 0 ? 2 * u.c0 + u.odd : 2 * (u.c0 + s)) * (NQ * kRows) + rr; };
-    float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) M = fmaxf(M, P.part_ml[row_of(s) * 2]);
+    auto part = [&](int s) { return (int64_t)(s == 0 ? 2 * u.c0 + u.odd : 2 * (u.c0 + s)) * NQ + q; };
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int B = 8;                                      // pieces in flight
+    for (int s0 = 0; s0 < n; s0 += B) {
+        float2 ml[B];
+        float4 o[B];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[PER], den = 0.f;
+        for (int k = 0; k < B; ++k) {
+            const int64_t p = part(min(s0 + k, n - 1));
+            ml[k] = P.part_ml[p * kRows + r];
+            o[k] = P.part_o[(p * (HD / 4) + col) * kRows + r];
+        }
+        float top = M;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-    for (int s = 0; s < n; ++s) {
-        const float2 ml = *reinterpret_cast<const float2*>(P.part_ml + row_of(s) * 2);
-        const float w = ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
-        den += w;
-        const float* o = P.part_o + row_of(s) * HD + lane;
+        for (int k = 0; k < B; ++k) top = fmaxf(top, ml[k].x);
+        const float f = M == -INFINITY ? 0.f : ex2(M - top);
+        M = top;
+        den *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] = fmaf(w, o[32 * k], acc[k]);
+        for (int k = 0; k < B; ++k) {
+            const float w = s0 + k >= n || ml[k].x == -INFINITY ? 0.f : ml[k].y * ex2(ml[k].x - M);
+            den += w;
+            acc.x = fmaf(w, o[k].x, acc.x); acc.y = fmaf(w, o[k].y, acc.y); acc.z = fmaf(w, o[k].z, acc.z); acc.w = fmaf(w, o[k].w, acc.w);
+        }
     }
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    T* out = static_cast<T*>(P.a.out) + (int64_t)(req.t0 + i) * P.a.out_stride + (int64_t)h * HD + lane;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) out[32 * k] = from_f<T>(acc[k] * inv);
-    if (P.a.lse && lane == 0) P.a.lse[(int64_t)(req.t0 + i) * P.a.nH + h] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+    T* out = static_cast<T*>(P.a.out) + (int64_t)(req.t0 + i) * P.a.out_stride + (int64_t)h * HD + col * 4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    if (P.a.lse && col == 0) P.a.lse[(int64_t)(req.t0 + i) * P.a.nH + h] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host
 PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
 std::once_flag g_enc_once;
 
-bool make_map(CUtensorMap* tm, const void* ptr, int dtype, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+template <int RANK>
+bool make_map(CUtensorMap* tm, const void* ptr, int dtype, const cuuint64_t (&dims)[RANK], const cuuint64_t (&strides)[RANK - 1], const cuuint32_t (&box)[RANK]) {
     std::call_once(g_enc_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -742,7 +868,8 @@ bool make_map(CUtensorMap* tm, const void* ptr, int dtype, const cuuint64_t (&di
     });
     if (!g_enc) return false;
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return g_enc(tm, dtype == DSPARK_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+    static_assert(RANK <= 4, "element strides");
+    return g_enc(tm, dtype == DSPARK_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK,
                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -772,9 +899,10 @@ cudaError_t launch(Params P, cudaStream_t s) {
     const cuuint64_t qd[4] = {(cuuint64_t)a.hd, (cuuint64_t)a.grp, (cuuint64_t)a.nKv, (cuuint64_t)a.T};
     const cuuint64_t qs[3] = {hb, hb * a.grp, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t qb[4] = {64, (cuuint32_t)a.grp, 1, (cuuint32_t)P.tpt};
-    const cuuint64_t kd[4] = {(cuuint64_t)a.hd, (cuuint64_t)a.nKv, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages};
-    const cuuint64_t ks[3] = {hb, hb * a.nKv, hb * a.nKv * a.page_size};
-    const cuuint32_t kb[4] = {64, 1, (cuuint32_t)std::min(a.page_size, C::KT), 1};
+    // (a page is page_size rows of all kv heads: the fewer dimensions, the faster small boxes go)
+    const cuuint64_t kd[2] = {(cuuint64_t)a.nKv * a.hd, (cuuint64_t)a.num_pages * a.page_size};
+    const cuuint64_t ks[1] = {hb * a.nKv};
+    const cuuint32_t kb[2] = {64, (cuuint32_t)std::min(a.page_size, C::KT)};
     if (!make_map(&tq, a.q, a.dtype, qd, qs, qb) || !make_map(&tk, a.k, a.dtype, kd, ks, kb) || !make_map(&tv, a.v, a.dtype, kd, ks, kb))
         return cudaErrorInvalidValue;
     auto kern = attend_paged_tc_kernel<T, C>;
@@ -783,7 +911,7 @@ cudaError_t launch(Params P, cudaStream_t s) {
     e = launch_pdl(attend_paged_plan_kernel<C::KT>, dim3(1), dim3(kPlanThreads), (a.B + 1) * sizeof(int64_t), s, P);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(kGrid), dim3(C::kThreads), C::kSmem, s, tq, tk, tv, P);
     if (e == cudaSuccess)
-        e = launch_pdl(attend_paged_merge_kernel<T, C::HD, C::NQ>, dim3(kGrid, C::NQ * kRows / kMergeWarps), dim3(kMergeWarps * 32), 0, s, P);
+        e = launch_pdl(attend_paged_merge_kernel<T, C::HD, C::NQ>, dim3(kGrid, C::NQ * kRows / 32, C::HD / 4 / kMergeCols), dim3(32 * kMergeCols), 0, s, P);
     return e;
 }
 
@@ -804,7 +932,7 @@ cudaError_t dispatch(const Params& P, cudaStream_t s) {
 
 bool attend_paged_tc_supported(const dspark_paged_cache& c, int n_heads) {
     return c.dtype != DSPARK_DTYPE_F32 && c.head_dim % 64 == 0 && c.page_size >= 8 && (c.page_size & (c.page_size - 1)) == 0 &&
-           n_heads / c.n_kv <= kRows && (int64_t)c.page_size * c.n_kv * c.head_dim * 2 < ((int64_t)1 << 40);
+           n_heads / c.n_kv <= kRows && ((int64_t)c.num_pages + 1) * c.page_size < ((int64_t)1 << 31);
 }
 int attend_paged_max_batch() { return kMaxBatch; }
 size_t attend_paged_tc_workspace(int hd) { return layout(hd).total; }
@@ -816,8 +944,8 @@ cudaError_t launch_attend_paged_tc(const PagedAttn& a, void* ws, cudaStream_t s)
     P.a = a;
     P.shares = reinterpret_cast<Share*>(w + l.shares);
     P.merges = reinterpret_cast<MergeUnit*>(w + l.merges);
-    P.part_ml = reinterpret_cast<float*>(w + l.ml);
-    P.part_o = reinterpret_cast<float*>(w + l.o);
+    P.part_ml = reinterpret_cast<float2*>(w + l.ml);
+    P.part_o = reinterpret_cast<float4*>(w + l.o);
     P.status = a.status ? a.status : reinterpret_cast<int32_t*>(w + l.status);
     while ((1 << P.page_shift) < a.page_size) ++P.page_shift;
     return a.dtype == DSPARK_DTYPE_F16 ? dispatch<__half>(P, s) : dispatch<__nv_bfloat16>(P, s);
