@@ -22,8 +22,8 @@
 //
 // Work split: the units' tiles (plus kUnitCost a unit for its fixed work), laid end to
 // end, are cut into equal contiguous shares, one per CTA, whatever the
-// requests' lengths (which only the device knows): a plan kernel finds each share's
-// start and the units that a cut crosses. Those units' pieces write O / l (fp32) and (m, l)
+// requests' lengths (which only the device knows): each CTA finds its share's start, and the units that a cut crosses
+// are listed. Those units' pieces write O / l (fp32) and (m, l)
 // per row, which a merge kernel joins in order: results do not depend on timing.
 //
 // Warp roles: 8 softmax warps (TMEM lane = query row; NQ = 1: two threads to a row), then one warp
@@ -49,7 +49,6 @@ constexpr int kUnitCost = 2;         // a unit's fixed work (query tile, first l
 constexpr int kRows = 128;           // rows of a query tile: the MMAs' M
 constexpr int kMaxBatch = 4096;
 constexpr float kRescale = 8.0f;     // log2 headroom before the running maximum is raised
-constexpr int kPlanThreads = 512;
 constexpr size_t kSmemMax = 232448;
 
 struct Share { int b, g, qt, x; int64_t len; };          // first unit, offset in it, total length (cost units)
@@ -57,7 +56,7 @@ struct MergeUnit { int b, g, qt, c0, odd, c1; };         // pieces: slot 2 c0 + 
 
 struct Params {
     PagedAttn a;
-    Share* shares; MergeUnit* merges;
+    MergeUnit* merges;               // [kGrid]
     float4* part_o; float2* part_ml;  // [2 kGrid][NQ][hd / 4][128], [2 kGrid][NQ][128]
     int tpt, tpu;                    // tokens per query tile, per unit
     int page_shift;
@@ -105,8 +104,7 @@ struct Walk {
     int64_t rem;
     bool first, have;
     Req r;
-    __device__ __forceinline__ Walk(const Params& P, int cta) {
-        const Share s = P.shares[cta];
+    __device__ __forceinline__ Walk(const Share& s, int cta) {
         b = s.b; g = s.g; qt = s.qt; x = s.x; rem = s.len; c = cta; index = 0; first = true; have = false;
     }
     __device__ __forceinline__ bool next(const Params& P, Piece* p) {
@@ -152,17 +150,16 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------ plan
-// One block: the requests' costs and their prefix sums, then thread c places share c.
+// Every CTA finds its own share (a kernel before this one would cost more than the few microseconds this takes): the
+// requests' costs and their prefix sums over the block, then warp 0 places the share. It also lists the unit, if any,
+// whose first cut between tiles is this share's start. pre: B + 1 numbers of scratch; buf: one per warp.
 template <int KT>
-__global__ void __launch_bounds__(kPlanThreads) attend_paged_plan_kernel(Params P) {
-    extern __shared__ int64_t s_pre[];                  // [B + 1] cost of the requests before b
-    __shared__ int64_t s_buf[kPlanThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, B = P.a.B;
-    pdl_trigger();
-    pdl_wait();
+__device__ __forceinline__ void plan_share(const Params& P, int64_t* pre, int64_t* buf, Share* share) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, B = P.a.B, threads = blockDim.x, warps = threads >> 5;
+    const int cta = blockIdx.x;
     // a request's cost: a thread per request for few units each, a warp for many
     const bool by_warp = P.a.max_new > 4 * P.tpu;
-    for (int b = by_warp ? wid : tid; b < B; b += by_warp ? kPlanThreads / 32 : kPlanThreads) {
+    for (int b = by_warp ? wid : tid; b < B; b += by_warp ? warps : threads) {
         const Req r = load_req(P.a, b);
         int64_t cost = 0;
         const int units = (r.n + P.tpu - 1) / P.tpu;
@@ -173,76 +170,90 @@ __global__ void __launch_bounds__(kPlanThreads) attend_paged_plan_kernel(Params 
             for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
         }
         if (!by_warp || lane == 0) {
-            s_pre[b] = cost;
-            if (P.a.kv_len[b] != r.L || P.a.cu[b] != r.t0 || P.a.cu[b + 1] != r.t0 + r.n) atomicOr(P.status, DSPARK_DEV_BAD_LENGTH);
+            pre[b] = cost;
+            if (cta == 0 && (P.a.kv_len[b] != r.L || P.a.cu[b] != r.t0 || P.a.cu[b + 1] != r.t0 + r.n)) atomicOr(P.status, DSPARK_DEV_BAD_LENGTH);
         }
     }
     __syncthreads();
     // exclusive prefix sums, a contiguous run of requests per thread
-    const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int per = (B + threads - 1) / threads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += s_pre[b] * P.a.nKv;
+    for (int b = b0; b < b1; ++b) mine += pre[b] * P.a.nKv;
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    if (lane == 31) s_buf[wid] = inc;
+    if (lane == 31) buf[wid] = inc;
     __syncthreads();
     int64_t base = 0, W = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < wid) base += s_buf[w];
-        W += s_buf[w];
+    for (int w = 0; w < warps; ++w) {
+        if (w < wid) base += buf[w];
+        W += buf[w];
     }
     base += inc - mine;
     for (int b = b0; b < b1; ++b) {
-        const int64_t cb = s_pre[b] * P.a.nKv;
-        s_pre[b] = base;
+        const int64_t cb = pre[b] * P.a.nKv;
+        pre[b] = base;
         base += cb;
     }
-    if (tid == 0) s_pre[B] = W;
+    if (tid == 0) pre[B] = W;
     __syncthreads();
-    // shares of at least kUnitCost + 1: below that a piece is all fixed work
-    const int64_t G = min((int64_t)kGrid, max((int64_t)1, W / (kUnitCost + 1)));
-    auto start = [&](int64_t c) { return c >= G ? W : W * c / G; };
-    if (tid >= kGrid) return;
-    const int64_t lo = start(tid), hi = start(tid + 1);
-    Share s{0, 0, 0, 0, hi - lo};
-    MergeUnit mu{0, 0, 0, 0, 0, -1};
-    if (hi > lo) {
-        int l = 0, h = B;                                // the last request that starts at or before lo and is not empty
-        while (h - l > 1) {
-            const int mid = (l + h) >> 1;
-            if (s_pre[mid] <= lo) l = mid; else h = mid;
+    if (wid == 0) {
+        // shares of at least kUnitCost + 1: below that a piece is all fixed work
+        const int64_t G = min((int64_t)kGrid, max((int64_t)1, W / (kUnitCost + 1)));
+        auto start = [&](int64_t c) { return c >= G ? W : W * c / G; };
+        const int64_t lo = start(cta), hi = start(cta + 1);
+        Share s{0, 0, 0, 0, hi - lo};
+        MergeUnit mu{0, 0, 0, 0, 0, -1};
+        if (hi > lo) {
+            int l = 0, h = B;                                // the last request that starts at or before lo and is not empty
+            while (h - l > 1) {
+                const int mid = (l + h) >> 1;
+                if (pre[mid] <= lo) l = mid; else h = mid;
+            }
+            const Req r = load_req(P.a, l);
+            const int64_t cg = (pre[l + 1] - pre[l]) / P.a.nKv;
+            int64_t rest = lo - pre[l];
+            s.b = l;
+            s.g = (int)(rest / cg);
+            rest -= s.g * cg;
+            int cost = 0;
+            for (int qt = 0;; qt += 32) {                    // 32 units at a time
+                const int mine = kUnitCost + unit_tiles<KT>(P.a, r, P.tpu, min(qt + lane, (r.n - 1) / P.tpu));
+                int64_t sum = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                const unsigned over = __ballot_sync(0xffffffffu, sum > rest);
+                if (over) {
+                    const int k = __ffs(over) - 1;
+                    s.qt = qt + k;
+                    cost = __shfl_sync(0xffffffffu, mine, k);
+                    s.x = (int)(rest - __shfl_sync(0xffffffffu, sum - mine, k));
+                    break;
+                }
+                rest -= __shfl_sync(0xffffffffu, sum, 31);
+            }
+            const int64_t u0 = lo - s.x;                     // where the unit starts
+            if (cta > 0 && s.x > kUnitCost && start(cta - 1) - u0 <= kUnitCost) {
+                mu.b = s.b; mu.g = s.g; mu.qt = s.qt;
+                mu.c0 = cta - 1;
+                mu.odd = start(cta - 1) < u0;                // not the first region of that share
+                int c1 = cta;
+                while (c1 + 1 < G && start(c1 + 1) < u0 + cost) ++c1;
+                mu.c1 = c1;
+            }
         }
-        const Req r = load_req(P.a, l);
-        const int64_t cg = (s_pre[l + 1] - s_pre[l]) / P.a.nKv;
-        int64_t rest = lo - s_pre[l];
-        s.b = l;
-        s.g = (int)(rest / cg);
-        rest -= s.g * cg;
-        int qt = 0, cost;
-        for (;; ++qt) {
-            cost = kUnitCost + unit_tiles<KT>(P.a, r, P.tpu, qt);
-            if (rest < cost) break;
-            rest -= cost;
-        }
-        s.qt = qt;
-        s.x = (int)rest;
-        // the cut at lo splits the unit's tiles, and is the first that does: this thread lists the unit
-        const int64_t u0 = lo - rest;                    // where the unit starts
-        if (tid > 0 && s.x > kUnitCost && start(tid - 1) - u0 <= kUnitCost) {
-            mu.b = s.b; mu.g = s.g; mu.qt = qt;
-            mu.c0 = tid - 1;
-            mu.odd = start(tid - 1) < u0;                // not the first region of that share
-            int c1 = tid;
-            while (c1 + 1 < G && start(c1 + 1) < u0 + cost) ++c1;
-            mu.c1 = c1;
+        if (lane == 0) {
+            *share = s;
+            P.merges[cta] = mu;
         }
     }
-    P.shares[tid] = s;
-    P.merges[tid] = mu;
+    __syncthreads();
 }
 
 // ------------------------------------------------------------------ PTX used here alone
@@ -285,7 +296,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 // 2^x for two x in [-126, 127) on the FMA pipe: the nearest integer goes into the exponent, 2^f on |f| <= 1/2 is a polynomial
 // of degree 5 fitted for the relative error (within 2^-23.6). The special function unit does 16
-// a clock, which is what a 128 x 128 tile's two products leave time for: a quarter of them here makes room.
+// a clock, which is what a 128 x 128 tile's two products leave time for: some of them here make room.
 __device__ __forceinline__ void exp2_poly(uint64_t x, float& p0, float& p1) {
     const uint64_t magic = f2(12582912.f, 12582912.f);          // 1.5 2^23: the sum's low bits are the integer
     const uint64_t t = add2(x, magic), n = add2(t, f2(-12582912.f, -12582912.f)), f = fma2(n, f2(-1.f, -1.f), x);
@@ -346,14 +357,15 @@ struct Cfg {
     static constexpr int kQSlots = QTMEM ? (NCH + kQPerSlot - 1) / kQPerSlot : 0;
     static constexpr int kOCol = 2 * KT, kQCol = 2 * KT + HD; // TMEM columns: S buffers, O tiles, Q
     static constexpr size_t kSmem = 1024 + kQBytes + (size_t)NS * kTile + kTail;
-    static_assert(kSmem <= kSmemMax, "shared memory");
+    static_assert(kSmem <= kSmemMax && (size_t)NS * kTile >= (kMaxBatch + 33) * 8, "shared memory");
     static_assert(2 * KT + NQ * HD + (QTMEM ? HD / 2 : 0) <= 512, "tensor memory");
 };
 
 struct Bars {
     uint64_t full[12], free_[12], vissued[12], vready[12];
-    uint64_t sdone[2], pready[2], odone[2];
+    uint64_t sdone[2], pready[2], phalf[2], odone[2];
     uint64_t qfull, qfree, spare;
+    Share share;
     uint32_t tmem;
     int abort;
 };
@@ -383,7 +395,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) { mbar_init(&B.full[i], 1); mbar_init(&B.free_[i], 1); mbar_init(&B.vissued[i], 1); mbar_init(&B.vready[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&B.sdone[i], 1); mbar_init(&B.pready[i], C::SP * 128); mbar_init(&B.odone[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&B.sdone[i], 1); mbar_init(&B.pready[i], C::SP * 128); mbar_init(&B.phalf[i], C::SP * 128); mbar_init(&B.odone[i], 1); }
         mbar_init(&B.qfull, C::QTMEM ? C::SP * 128 : 1);
         mbar_init(&B.qfree, 1);
         mbar_init(&B.spare, 1);
@@ -398,7 +410,11 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const uint32_t tmem = B.tmem;
     pdl_wait();
 
-    Walk<KT> walk(P, blockIdx.x);
+    int64_t* scratch = reinterpret_cast<int64_t*>(ring);
+    plan_share<KT>(P, scratch, scratch + kMaxBatch + 1, &B.share);
+    fence_async_shared();                                     // the ring was scratch: TMA writes it next
+    __syncthreads();
+    Walk<KT> walk(B.share, blockIdx.x);
     Piece p;
     int e = 0;                                                // ring entries before the piece
     int gs = 0;                                               // steps before the piece
@@ -539,13 +555,23 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     if (!__all_sync(0xffffffffu, wait(bar, par))) { ok = false; break; }
                     if (part) vpar ^= 1u << sl;
                 }
+                const uint32_t d = tmem + (uint32_t)(C::kOCol + q * HD), pa = tmem + (uint32_t)(buf * KT);
+                const uint64_t bd = sdesc_mn_sw128(ring0 + (uint32_t)sl * C::kTile, KT * 128);
+                constexpr int J0 = NQ == 2 ? 4 : 0;           // MMAs on the half of P that is ready first
+                if (NQ == 2) {
+                    if (!__all_sync(0xffffffffu, wait(&B.phalf[buf], (uint32_t)((g0 + s) >> 1) & 1u))) { ok = false; break; }
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int j = 0; j < J0; ++j)
+                            mma_f16_ts(d, pa + (uint32_t)(8 * j), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
+                    }
+                }
                 if (!__all_sync(0xffffffffu, wait(&B.pready[buf], (uint32_t)((g0 + s) >> 1) & 1u))) { ok = false; break; }
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t d = tmem + (uint32_t)(C::kOCol + q * HD), pa = tmem + (uint32_t)(buf * KT);
-                    const uint64_t bd = sdesc_mn_sw128(ring0 + (uint32_t)sl * C::kTile, KT * 128);
 #pragma unroll
-                    for (int j = 0; j < KT / 16; ++j)
+                    for (int j = J0; j < KT / 16; ++j)
                         mma_f16_ts(d, pa + (uint32_t)(j / (C::CH / 16) * C::CH + j % (C::CH / 16) * 8), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
                     mma_commit(&B.odone[buf]);
                     if (q == NQ - 1) mma_commit(&B.free_[sl]);
@@ -705,7 +731,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 const float neg = m == -INFINITY ? 0.f : -m;
                 const uint64_t c2 = f2(c, c), neg2 = f2(neg, neg);
                 uint64_t ls[2] = {0, 0};
-                // poly: a quarter of the exponentials on the FMA pipe (scores of -infinity have no place there)
+                // poly: an eighth of the exponentials on the FMA pipe (scores of -infinity have no place there)
                 auto exps = [&](int j0, auto poly) {
 #pragma unroll
                     for (int j = 0; j < W; j += 16) {
@@ -715,7 +741,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                             const uint64_t x = fma2(f2(__uint_as_float(u[j + i]), __uint_as_float(u[j + i + 1])), c2, neg2);
                             float p0, p1, x0, x1;
                             f2_out(x, x0, x1);
-                            if (poly.value && (i & 6) == 6) {
+                            if (poly.value && (i & 14) == 14) {
                                 exp2_poly(f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f)), p0, p1);
                             } else {
                                 p0 = ex2(x0);
@@ -731,7 +757,13 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 for (int j = 0; j < CH && live; j += W) {
                     if (j > 0) fetch(j);
                     if (edge) exps(j, std::false_type{}); else exps(j, std::true_type{});
+                    if (SP == 1 && j == 0) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&B.phalf[buf]);
+                    }
                 }
+                if (SP == 1 && !live) mbar_arrive(&B.phalf[buf]);
                 float l0, l1;
                 f2_out(add2(ls[0], ls[1]), l0, l1);
                 l += l0 + l1;
@@ -874,14 +906,13 @@ bool make_map(CUtensorMap* tm, const void* ptr, int dtype, const cuuint64_t (&di
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Layout { size_t status, shares, merges, ml, o, total; };
+struct Layout { size_t status, merges, ml, o, total; };
 Layout layout(int hd) {
     const int rows = hd <= 128 ? 2 * kRows : kRows;
     Layout l{};
     size_t at = 0;
     auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
     l.status = take(4);
-    l.shares = take(kGrid * sizeof(Share));
     l.merges = take(kGrid * sizeof(MergeUnit));
     l.ml = take((size_t)2 * kGrid * rows * 2 * sizeof(float));
     l.o = take((size_t)2 * kGrid * rows * hd * sizeof(float));
@@ -908,8 +939,7 @@ cudaError_t launch(Params P, cudaStream_t s) {
     auto kern = attend_paged_tc_kernel<T, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_paged_plan_kernel<C::KT>, dim3(1), dim3(kPlanThreads), (a.B + 1) * sizeof(int64_t), s, P);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(kGrid), dim3(C::kThreads), C::kSmem, s, tq, tk, tv, P);
+    e = launch_pdl(kern, dim3(kGrid), dim3(C::kThreads), C::kSmem, s, tq, tk, tv, P);
     if (e == cudaSuccess)
         e = launch_pdl(attend_paged_merge_kernel<T, C::HD, C::NQ>, dim3(kGrid, C::NQ * kRows / 32, C::HD / 4 / kMergeCols), dim3(32 * kMergeCols), 0, s, P);
     return e;
@@ -942,7 +972,6 @@ cudaError_t launch_attend_paged_tc(const PagedAttn& a, void* ws, cudaStream_t s)
     char* w = static_cast<char*>(ws);
     Params P{};
     P.a = a;
-    P.shares = reinterpret_cast<Share*>(w + l.shares);
     P.merges = reinterpret_cast<MergeUnit*>(w + l.merges);
     P.part_ml = reinterpret_cast<float2*>(w + l.ml);
     P.part_o = reinterpret_cast<float4*>(w + l.o);
