@@ -311,6 +311,22 @@ __device__ __forceinline__ void exp2_poly(uint64_t x, float& p0, float& p1) {
     p0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23));
     p1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
 }
+// Lane j of four has blocks 0 .. 3 (four words each) of row j; after this, block j of rows 0 .. 3.
+__device__ __forceinline__ void transpose_blocks(uint32_t (&w)[16], int lane) {
+#pragma unroll
+    for (int x = 1; x <= 2; x *= 2) {
+        const bool odd = lane & x;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (b & x) continue;                              // blocks b and b + x
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t t = __shfl_xor_sync(0xffffffffu, odd ? w[4 * b + i] : w[4 * (b + x) + i], x);
+                if (odd) w[4 * b + i] = t; else w[4 * (b + x) + i] = t;
+            }
+        }
+    }
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -604,9 +620,11 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 if (!__all_sync(0xffffffffu, in)) { ok = false; break; }
                 uint8_t* tile = ring + (size_t)sl * C::kTile;
                 const int dead = KT - (b - a);
-                for (int i = lane; i < NCH * dead * 8; i += 32) {
-                    const int c = i / (dead * 8), rest = i - c * (dead * 8), row = rest >> 3;
-                    *reinterpret_cast<uint4*>(tile + c * (KT * 128) + (row < a ? row : row - a + b) * 128 + (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = lane; i < dead * 8; i += 32) {
+                    const int row = i >> 3;
+                    uint8_t* line = tile + (row < a ? row : row - a + b) * 128 + (i & 7) * 16;
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) *reinterpret_cast<uint4*>(line + c * (KT * 128)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_shared();                         // the MMAs read through the async proxy
                 __syncwarp();
@@ -630,7 +648,36 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         };
         auto agree = [&](bool good) { return SP == 1 ? good : !named_barrier_or(1, 256, !good); };   // a row's threads meet; false if one gave up
         const int grp = P.a.grp, tok_r = r / grp, head_r = r - tok_r * grp;
-        while (ok && walk.next(P, &p)) {
+        // The loaded query rows of a piece (ring entries from e0) into tensor memory, two 16-bit values per column; the S
+        // products of the piece before have all completed (their last was waited for).
+        auto stage = [&](int e0) {
+            const bool filled = r < P.tpt * grp;
+            for (int s = 0; s < C::kQSlots; ++s) {
+                const int en = e0 + s, sl = en % NS;
+                if (!wait(&B.full[sl], (uint32_t)(en / NS) & 1u)) return false;
+                const int c0 = s * C::kQPerSlot, c1 = min(NCH, c0 + C::kQPerSlot);
+                for (int cc = c0; cc < c1; ++cc) {
+                    const uint8_t* line = ring + (size_t)sl * C::kTile + (cc - c0) * C::kChunk + r * 128;
+                    static_assert(!C::QTMEM || SP == 2, "each thread of a row stages half a line");
+                    const int j0 = 4 * half;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (filled) u = *reinterpret_cast<const uint4*>(line + (((j0 + j) ^ (r & 7)) * 16));
+                        w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+                    }
+                    tmem_st_x16(tmem + (uint32_t)(C::kQCol + cc * 32 + j0 * 4) + lane_off, w);
+                }
+            }
+            tmem_st_wait();
+            fence_async_shared();                             // reads done before the slots are loaded again
+            tc_fence_before();
+            mbar_arrive(&B.qfull);                            // the MMA warp then frees the slots
+            return true;
+        };
+        bool more = walk.next(P, &p), staged = false;
+        while (ok && more) {
             const int i = p.qt * P.tpu + q * P.tpt + tok_r;   // this row's token of the request
             const bool valid = tok_r < P.tpt && i < p.r.n;
             const int pos = p.r.L - p.r.n + i;
@@ -642,35 +689,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             const int all_lo = P.a.window > 0 ? max(0, p.r.L - p.r.n + i_last - P.a.window + 1) : 0;
             const bool live = __any_sync(0xffffffffu, valid);  // the warp has a row to compute (the MMAs read garbage for the others)
             float m = -INFINITY, l = 0.f;
-            if (C::QTMEM && p.nt > 0) {
-                // the staged query rows into tensor memory, two 16-bit values per column; the S products of
-                // the piece before have all completed (their last was waited for)
-                const bool filled = r < P.tpt * grp;
-                for (int s = 0; s < C::kQSlots && ok; ++s) {
-                    const int en = e + s, sl = en % NS;
-                    if (!wait(&B.full[sl], (uint32_t)(en / NS) & 1u)) { ok = false; break; }
-                    const int c0 = s * C::kQPerSlot, c1 = min(NCH, c0 + C::kQPerSlot);
-                    for (int cc = c0; cc < c1; ++cc) {
-                        const uint8_t* line = ring + (size_t)sl * C::kTile + (cc - c0) * C::kChunk + r * 128;
-                        static_assert(!C::QTMEM || SP == 2, "each thread of a row stages half a line");
-                        const int j0 = 4 * half;
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                            if (filled) u = *reinterpret_cast<const uint4*>(line + (((j0 + j) ^ (r & 7)) * 16));
-                            w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
-                        }
-                        tmem_st_x16(tmem + (uint32_t)(C::kQCol + cc * 32 + j0 * 4) + lane_off, w);
-                    }
-                }
-                if (ok) {
-                    tmem_st_wait();
-                    fence_async_shared();                     // reads done before the slots are loaded again
-                    tc_fence_before();
-                    mbar_arrive(&B.qfull);                    // the MMA thread then frees the slots
-                }
-            }
+            if (C::QTMEM && p.nt > 0 && !staged) ok = stage(e);
             bool good = ok;
             int last_step = -1;
             for (int t = 0; t < p.nt; ++t) {
@@ -774,41 +793,48 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             }
             // ---- the piece's result
             if (!ok) break;                                   // (all of the tile's warps)
-            if (p.nt > 0) good = good && wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u);
+            // the next piece's queries first: its S products run beside this epilogue
+            const Piece now = p;
+            more = walk.next(P, &p);
+            staged = C::QTMEM && more && p.nt > 0;
+            if (staged) good = stage(e + (now.nt > 0 ? C::kQSlots + 2 * now.nt : 0)) && good;
+            if (now.nt > 0) good = good && wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u);
             tc_fence_after();
-            if (SP == 2) mine[(p.nt & 1) * 256] = l;
+            if (SP == 2) mine[(now.nt & 1) * 256] = l;
             if (!agree(good)) { ok = false; break; }
             if (SP == 2) {
-                l += other[(p.nt & 1) * 256];
+                l += other[(now.nt & 1) * 256];
                 named_barrier_sync(1, 256);                   // both have read: the next piece may write
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int64_t tok = p.r.t0 + i;
-            const int h = p.g * grp + head_r;
-            if (p.whole) {
-                T* out = static_cast<T*>(P.a.out) + tok * P.a.out_stride + (int64_t)h * HD + half * OH;
+            const int64_t tok = now.r.t0 + i;
+            const int h = now.g * grp + head_r;
+            if (now.whole) {
+                // A store of one row per lane would touch 32 lines. Four lanes exchange 16-byte blocks instead, so that
+                // they write 64 bytes of one of their rows at a time.
+                const int64_t at = valid ? tok * P.a.out_stride + (int64_t)h * HD + half * OH : -1;
+                int64_t row_at[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) row_at[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+                T* out = static_cast<T*>(P.a.out) + (lane & 3) * 8;
 #pragma unroll
                 for (int d = 0; d < OH; d += 32) {
-                    uint32_t o[32];
-                    if (p.nt > 0) {
+                    uint32_t o[32], w[16];
+                    if (now.nt > 0) {
                         tmem_ld_x32(tO + (uint32_t)d, o);
                         tmem_ld_wait();
                     }
-                    if (valid) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint32_t w[4];
+                    for (int j = 0; j < 16; ++j) w[j] = l > 0.f ? pack2<T>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv) : 0u;
+                    transpose_blocks(w, lane);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = l > 0.f ? pack2<T>(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv) : 0u;
-                            *reinterpret_cast<uint4*>(out + d + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        if (row_at[k] >= 0) *reinterpret_cast<uint4*>(out + row_at[k] + d) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                 }
                 if (valid && half == 0 && P.a.lse) P.a.lse[tok * P.a.nH + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
             } else {
                 // [slot][column / 4][row] float4: a warp's rows are neighbours
-                const int64_t part = (int64_t)p.slot * NQ + q;
+                const int64_t part = (int64_t)now.slot * NQ + q;
                 if (valid && half == 0) P.part_ml[part * kRows + r] = make_float2(l > 0.f ? m : -INFINITY, l);
                 float4* po = P.part_o + (part * (HD / 4) + half * (OH / 4)) * kRows + r;
 #pragma unroll
@@ -825,9 +851,9 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 }
             }
             tc_fence_before();                                // O read before the next piece's first PV (behind its P)
-            if (p.nt > 0) {
-                e += C::kQSlots + 2 * p.nt;
-                gs += p.nt * NQ;
+            if (now.nt > 0) {
+                e += C::kQSlots + 2 * now.nt;
+                gs += now.nt * NQ;
             }
         }
     }
@@ -840,7 +866,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 // ------------------------------------------------------------------ merge
 // out = sum_s w_s O_s / sum_s w_s, w_s = l_s exp2(m_s - M), over a unit's pieces in order. A thread has four columns
 // of a row, neighbouring threads neighbouring rows (as the pieces lie): grid (units, row groups, column groups).
-constexpr int kMergeCols = 8;                                 // float4 columns per block
+constexpr int kMergeCols = 16;                                // float4 columns per block
 template <typename T, int HD, int NQ>
 __global__ void __launch_bounds__(32 * kMergeCols) attend_paged_merge_kernel(Params P) {
     pdl_trigger();
