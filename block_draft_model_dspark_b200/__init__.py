@@ -261,33 +261,34 @@ def _refuse(msg: str):
 
 
 def _vec(t, name: str, dtype, n: int, dev: int):
-    """Checks a contiguous 1-d device array of at least n entries; returns its address."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(f"{name} must be a contiguous {dtype} tensor of at least {n} entries on cuda:{dev}")
-    return t.data_ptr()
+    """Checks a contiguous device array of at least n entries; returns its address."""
+    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(f"{name} must be a contiguous {dtype} tensor of at least {n} entries on cuda:{dev}")
 
 
-class _on:
-    """Makes the tensors' device current around a call when it is not, and gives the stream's address."""
-    __slots__ = ("dev", "stream", "prev")
+def _launch(fn, dev: int, stream, *args):
+    """fn(*args, stream) with the tensors' device current, on `stream` or the device's current one."""
+    import torch
+    c = torch._C
+    s = stream.cuda_stream if stream is not None else c._cuda_getCurrentRawStream(dev)
+    cur = c._cuda_getDevice()
+    if cur == dev:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != DSPARK_OK:
+        _check(rc)
 
-    def __init__(self, dev: int, stream):
-        self.dev, self.stream, self.prev = dev, stream, None
 
-    def __enter__(self):
-        import torch
-        cur = torch.cuda.current_device()
-        if cur != self.dev:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-        if self.stream is not None:
-            return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            import torch
-            torch.cuda.set_device(self.prev)
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the device's current one): its memory belongs to that stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class PagedKvCache:
@@ -343,22 +344,23 @@ def page_slots(cache: PagedKvCache, ctx_len, n_new, n_pages, free_pages, free_co
     ``free_count`` int32 [1]. Missing outputs are allocated (n_pages_out = n_pages and the like update in
     place); returns (cu_new, kv_len, slots, positions, n_pages_out, free_count_out)."""
     import torch
+    if ctx_len.dim() != 1:
+        _refuse("ctx_len must be one-dimensional")
     i32, B, dev = torch.int32, ctx_len.shape[0], cache.dev
-    new = lambda n, dt=i32: torch.empty(n, dtype=dt, device=cache.device)  # noqa: E731
+    new = lambda n, dt=i32: _empty(n, dt, cache.device, stream)  # noqa: E731
     n_pages_out = new(B) if n_pages_out is None else n_pages_out
     free_count_out = new(1) if free_count_out is None else free_count_out
     cu_new = new(B + 1) if cu_new is None else cu_new
     kv_len = new(B) if kv_len is None else kv_len
     slots = new(max_tokens, torch.int64) if slots is None else slots
     positions = new(max_tokens) if positions is None else positions
-    with _on(dev, stream) as s:
-        _check(get_lib().dspark_page_slots(
+    _launch(get_lib().dspark_page_slots, dev, stream,
             cache.ref, _vec(ctx_len, "ctx_len", i32, B, dev), _vec(n_new, "n_new", i32, B, dev), B,
-            _vec(n_pages, "n_pages", i32, B, dev), _vec(free_pages, "free_pages", i32, 0, dev), free_pages.shape[0],
+            _vec(n_pages, "n_pages", i32, B, dev), _vec(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
             _vec(free_count, "free_count", i32, 1, dev), max_tokens, _vec(n_pages_out, "n_pages_out", i32, B, dev),
             _vec(free_count_out, "free_count_out", i32, 1, dev), _vec(cu_new, "cu_new", i32, B + 1, dev),
             _vec(kv_len, "kv_len", i32, B, dev), _vec(slots, "slots", torch.int64, max_tokens, dev),
-            _vec(positions, "positions", i32, max_tokens, dev), s))
+            _vec(positions, "positions", i32, max_tokens, dev))
     return cu_new, kv_len, slots, positions, n_pages_out, free_count_out
 
 
@@ -386,17 +388,16 @@ def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: 
     if k.dtype is not dt or k.shape[0] < T or (v is not None and (v.dtype is not dt or v.shape[0] < T)):
         _refuse("q, k and v must have one dtype and the same tokens")
     if q_out is None:
-        q_out = torch.empty(T, nH, hd, dtype=cache.dtype, device=cache.device)
+        q_out = _empty((T, nH, hd), cache.dtype, cache.device, stream)
     elif q_out.dtype is not cache.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != dev:
         _refuse("q_out must be a contiguous [T, heads, head_dim] tensor in the cache's dtype")
-    with _on(dev, stream) as s:
-        _check(get_lib().dspark_norm_rope_paged(
+    _launch(get_lib().dspark_norm_rope_paged, dev, stream,
             cache.ref, layer, _dtype_code(dt), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, nH,
             _vec(q_norm, "q_norm", dt, hd, dev) if q_norm is not None else None,
             _vec(k_norm, "k_norm", dt, hd, dev) if k_norm is not None else None,
             _vec(inv_freq, "inv_freq", torch.float64, hd // 2, dev), eps, 1 if v_norm else 0,
             _vec(positions, "positions", torch.int32, T, dev), _vec(slots, "slots", torch.int64, T, dev), T,
-            q_out.data_ptr(), s))
+            q_out.data_ptr())
     return q_out
 
 
@@ -410,11 +411,11 @@ def rope_inv_freq(head_dim: int, theta: float = 1e6, partial_rotary_factor: floa
     return f.to(device)
 
 
-def attend_paged_workspace(cache: PagedKvCache, T: int, n_heads: int, B: int):
+def attend_paged_workspace(cache: PagedKvCache, T: int, n_heads: int, B: int, stream=None):
     """A workspace for ``attend_paged`` calls of up to T tokens and B requests."""
     import torch
     n = get_lib().dspark_attend_paged_workspace_bytes(cache.ref, T, n_heads, B)
-    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=cache.device)
+    return _empty(max(int(n), 256), torch.uint8, cache.device, stream)
 
 
 def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: int, scale: float, causal: bool = True,
@@ -424,12 +425,14 @@ def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: in
     gives them, ``max_new`` the most new tokens of a request. Returns out [T, nH, hd]; ``lse`` float32
     [T, nH] is filled if given."""
     import torch
-    dev, T, nH, B = cache.dev, q.shape[0], q.shape[1], kv_len.shape[0]
+    if q.dim() != 3 or kv_len.dim() != 1:
+        _refuse("q must be [T, heads, head_dim] and kv_len one-dimensional")
+    (T, nH, _), dev, B = q.shape, cache.dev, kv_len.shape[0]
     qs = _heads(q, "q", None, cache.head_dim, dev)
     if q.dtype is not cache.dtype:
         _refuse("q must be in the cache's dtype")
     if out is None:
-        out = torch.empty(T, nH, cache.head_dim, dtype=cache.dtype, device=cache.device)
+        out = _empty((T, nH, cache.head_dim), cache.dtype, cache.device, stream)
     elif out.dtype is not cache.dtype or out.shape != q.shape:
         _refuse("out must have q's shape and the cache's dtype")
     os_ = _heads(out, "out", nH, cache.head_dim, dev)
@@ -437,19 +440,18 @@ def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: in
                             lse.get_device() != dev):
         _refuse("lse must be a contiguous float32 tensor [T, heads]")
     if ws is None:
-        ws = attend_paged_workspace(cache, T, nH, B)
-    with _on(dev, stream) as s:
-        _check(get_lib().dspark_attend_paged(
+        ws = attend_paged_workspace(cache, T, nH, B, stream)
+    _launch(get_lib().dspark_attend_paged, dev, stream,
             cache.ref, layer, q.data_ptr(), qs, nH, _vec(cu_new, "cu_new", torch.int32, B + 1, dev),
             _vec(kv_len, "kv_len", torch.int32, B, dev), B, T, max_new, scale, 1 if causal else 0, window, out.data_ptr(),
-            os_, _ptr(lse), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), s))
+            os_, _ptr(lse), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
     return out
 
 
-def sample_workspace(rows: int, vocab: int, device="cuda"):
+def sample_workspace(rows: int, vocab: int, device="cuda", stream=None):
     """A workspace for ``sample`` calls of up to this many rows and entries."""
     import torch
-    return torch.empty(max(int(get_lib().dspark_sample_workspace_bytes(rows, vocab)), 256), dtype=torch.uint8, device=device)
+    return _empty(max(int(get_lib().dspark_sample_workspace_bytes(rows, vocab)), 256), torch.uint8, device, stream)
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, ws=None, stream=None):
@@ -462,17 +464,16 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
         _refuse("logits must be a CUDA tensor [rows, vocab] with contiguous rows")
     R, V = logits.shape
     if tokens is None:
-        tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
+        tokens = _empty(R, torch.int32, logits.device, stream)
     if ws is None:
-        ws = sample_workspace(R, V, logits.device)
-    with _on(dev, stream) as s:
-        _check(get_lib().dspark_sample(
+        ws = sample_workspace(R, V, logits.device, stream)
+    _launch(get_lib().dspark_sample, dev, stream,
             logits.data_ptr(), _dtype_code(logits.dtype), logits.stride(0), R, V, _vec(u, "u", f32, R, dev),
             None if temperature is None else _vec(temperature, "temperature", f32, R, dev),
             None if top_k is None else _vec(top_k, "top_k", torch.int32, R, dev),
             None if top_p is None else _vec(top_p, "top_p", f32, R, dev),
             None if min_p is None else _vec(min_p, "min_p", f32, R, dev), _vec(tokens, "tokens", torch.int32, R, dev),
-            None if probs is None else _vec(probs, "probs", f32, R, dev), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), s))
+            None if probs is None else _vec(probs, "probs", f32, R, dev), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
     return tokens
 
 

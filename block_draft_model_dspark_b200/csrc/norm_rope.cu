@@ -4,18 +4,23 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain          (v: no gain, or v as it is)
 //   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a),  a = position * inv_freq[i]
 // over the pairs (i, i + hd / 2). Bound by HBM: every element is read once and
-// written once. A thread owns eight consecutive elements of the head's first
+// written once. A warp has the heads of one token (or a share of them when there are few
+// tokens); `lanes` threads make a head, each with eight consecutive elements of its first
 // half and the eight they turn with (two 16-byte loads of 16-bit rows), so the
-// rotation needs no exchange; the sum of squares is a shuffle over the head's
-// lanes. The angles are one table per token in shared memory, shared by its
-// heads: the turn count is reduced in 64 bits (at position 10^6 a 32-bit angle
-// is off by 0.03 rad), sine and cosine are taken of the fraction in 32 bits.
+// rotation needs no exchange and its eight cosines and sines stay in registers from head to head; the sum of squares is
+// a shuffle over the head's lanes. The angles: the turn count is reduced in 64 bits (at position 10^6 a 32-bit angle
+// is off by 0.03 rad), sine and cosine are taken of the fraction in 32 bits, each once a warp.
 #include "paged.h"
 
 namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
+// Heads of a thread whose loads are in flight together, and the blocks an SM has registers for. Measured: 16384 tokens of 48
+// bf16 heads of 128 take 90 us so, 97 to 147 us with three or four heads, or the next round's loads ahead (registers);
+// fp32 rows (twice the bytes a load) gain from two heads what a third block gives.
+constexpr int kItems = 2;
+template <typename X> constexpr int kBlocksOf = sizeof(X) == 4 ? 2 : 3;
 
 struct NormRopeParams {
     const void* q; const void* k; const void* v; const void* q_norm; const void* k_norm;
@@ -24,7 +29,7 @@ struct NormRopeParams {
     void* q_out; void* kc; void* vc;
     int32_t* status;
     int64_t num_slots;
-    int T, nH, nKv, hd, lanes, v_norm, tokens;  // lanes: threads per head (a power of two); tokens: per block
+    int T, nH, nKv, hd, lanes, v_norm, split;   // lanes: threads per head (a power of two, at most 16); split: warps per token
     float eps;
 };
 
@@ -71,92 +76,112 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
 }
 
 template <typename X, typename O>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams P) {
-    extern __shared__ float2 s_rot[];           // [tokens][hd / 2] (cos, sin)
-    const int tid = threadIdx.x, half = P.hd / 2;
-    const int t0 = blockIdx.x * P.tokens, nt = min(P.tokens, P.T - t0);
+__global__ void __launch_bounds__(kThreads, kBlocksOf<X>) norm_rope_kernel(NormRopeParams P) {
+    const int lane = threadIdx.x & 31, half = P.hd / 2, groups = 32 / P.lanes;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
-    for (int i = tid; i < nt * half; i += kThreads) {
-        const int t = i / half, j = i - t * half;
-        // turns = position * inv_freq / (2 pi), whole turns dropped in 64 bits
-        const double turns = (double)P.positions[t0 + t] * P.inv_freq[j] * 0.15915494309189533576888376337251;
-        float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-        s_rot[i] = make_float2(c, s);
-    }
-    __syncthreads();
-    const int heads = P.nH + 2 * P.nKv, groups = kThreads / P.lanes;
-    const int grp = tid / P.lanes, l = tid % P.lanes, e = l * 8;
+    const int t = (int)(w / P.split), part = (int)(w - (int64_t)t * P.split);
+    if (t >= P.T) return;
+    const int grp = lane / P.lanes, l = lane % P.lanes, e = l * 8;
     const bool mine = e < half;                 // hd = 192 and the like leave lanes idle
-    const int items = nt * heads;
-    for (int it0 = 0; it0 < items; it0 += groups) {
-        const int it = it0 + grp;
-        int t = 0, h = 0;
-        int64_t slot = -1;
-        if (it < items) {
-            t = it / heads;
-            h = it - t * heads;
-            slot = P.slots[t0 + t];
+    const int heads = P.nH + 2 * P.nKv;
+    int64_t slot = P.slots[t];
+    const X* q = static_cast<const X*>(P.q) + t * P.q_stride + e;
+    const X* k = static_cast<const X*>(P.k) + t * P.k_stride + e;
+    const X* v = static_cast<const X*>(P.v) + t * P.v_stride + e;
+    const double pos = (double)P.positions[t];
+    float cs[8], sn[8];
+    bool ready = false;
+    for (int i0 = part * groups + grp; i0 - grp < heads; i0 += P.split * groups * kItems) {
+        // loads first, so that (the first time) the angles hide behind them
+        Raw8<X> r1[kItems], r2[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int h = i0 + i * P.split * groups;
+            if (h >= heads || !mine) continue;
+            const X* src = h < P.nH ? q + h * P.hd : h < P.nH + P.nKv ? k + (h - P.nH) * P.hd : v + (h - P.nH - P.nKv) * P.hd;
+            load8(r1[i], src);
+            load8(r2[i], src + half);
+        }
+        if (!ready) {
+            ready = true;
             if (slot >= P.num_slots) {
-                set_status(P.status, DSPARK_DEV_CAPACITY);
+                if (lane == 0) set_status(P.status, DSPARK_DEV_CAPACITY);
                 slot = -1;
             }
-        }
-        const bool on = slot >= 0 && mine;      // a negative slot is a padding row
-        const int kind = h < P.nH ? 0 : h < P.nH + P.nKv ? 1 : 2;
-        const int hh = kind == 0 ? h : kind == 1 ? h - P.nH : h - P.nH - P.nKv;
-        const X* src = kind == 0 ? static_cast<const X*>(P.q) + (t0 + t) * P.q_stride
-                     : kind == 1 ? static_cast<const X*>(P.k) + (t0 + t) * P.k_stride
-                                 : static_cast<const X*>(P.v) + (t0 + t) * P.v_stride;
-        src += (int64_t)hh * P.hd + e;
-        float x1[8], x2[8];
-        float ss = 0.f;
-        if (on) {
-            Raw8<X> r1, r2;
-            load8(r1, src);
-            load8(r2, src + half);
-            unpack8(r1, x1);
-            unpack8(r2, x2);
+            if (slot < 0) return;               // a padding row
+            // a lane's eight pairs: its group finds 8 / groups of them, the groups tell each other
+            const int each = groups >= 8 ? 1 : 8 / groups;    // 1, 2 or 4
+            float c[4], s[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x1[i] * x1[i] + x2[i] * x2[i];
-        }
-        for (int o = P.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!on) continue;                      // lanes of a head agree except idle ones; the shuffle is behind
-        const float r = kind == 2 && !P.v_norm ? 1.f : 1.f / sqrtf(ss / (float)P.hd + P.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) { x1[i] *= r; x2[i] *= r; }
-        if (kind < 2) {
-            const X* gain = static_cast<const X*>(kind == 0 ? P.q_norm : P.k_norm);
-            if (gain) {
-                Raw8<X> r1, r2;
-                float g1[8], g2[8];
-                load8(r1, gain + e);
-                load8(r2, gain + e + half);
-                unpack8(r1, g1);
-                unpack8(r2, g2);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) { x1[i] *= g1[i]; x2[i] *= g2[i]; }
+            for (int n = 0; n < 4; ++n) {
+                c[n] = 1.f;
+                s[n] = 0.f;
+                const int j = e + ((grp * each + n) & 7);
+                if (n >= each || j >= half) continue;
+                // turns = position * inv_freq / (2 pi), whole turns dropped in 64 bits
+                const double turns = pos * P.inv_freq[j] * 0.15915494309189533576888376337251;
+                sincospif((float)(2.0 * (turns - rint(turns))), &s[n], &c[n]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 cs = s_rot[t * half + e + i];
-                const float a = x1[i], b = x2[i];
-                x1[i] = a * cs.x - b * cs.y;
-                x2[i] = b * cs.x + a * cs.y;
+                const int from = i / each * P.lanes + l;
+                const float ci = each == 4 ? c[i & 3] : each == 2 ? c[i & 1] : c[0], si = each == 4 ? s[i & 3] : each == 2 ? s[i & 1] : s[0];
+                cs[i] = __shfl_sync(0xffffffffu, ci, from);
+                sn[i] = __shfl_sync(0xffffffffu, si, from);
             }
         }
-        O* dst = kind == 0 ? static_cast<O*>(P.q_out) + ((int64_t)(t0 + t) * P.nH + hh) * P.hd
-                           : static_cast<O*>(kind == 1 ? P.kc : P.vc) + (slot * P.nKv + hh) * P.hd;
-        store8(dst + e, x1);
-        store8(dst + e + half, x2);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int h = i0 + i * P.split * groups;
+            const bool on = h < heads && mine;
+            const int kind = h < P.nH ? 0 : h < P.nH + P.nKv ? 1 : 2;
+            float x1[8], x2[8];
+            float ss = 0.f;
+            if (on) {
+                unpack8(r1[i], x1);
+                unpack8(r2[i], x2);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss += x1[j] * x1[j] + x2[j] * x2[j];
+            }
+            for (int o = P.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (!on) continue;                  // lanes of a head agree except idle ones; the shuffle is behind
+            const float r = kind == 2 && !P.v_norm ? 1.f : 1.f / sqrtf(ss / (float)P.hd + P.eps);
+            if (kind == 2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) { x1[j] *= r; x2[j] *= r; }
+            } else {
+                const X* gain = static_cast<const X*>(kind == 0 ? P.q_norm : P.k_norm);      // (from L1: not worth its registers)
+                if (gain) {
+                    Raw8<X> w1, w2;
+                    float g1[8], g2[8];
+                    load8(w1, gain + e);
+                    load8(w2, gain + e + half);
+                    unpack8(w1, g1);
+                    unpack8(w2, g2);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) { x1[j] *= g1[j]; x2[j] *= g2[j]; }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float a = x1[j] * r, b = x2[j] * r;
+                    x1[j] = a * cs[j] - b * sn[j];
+                    x2[j] = b * cs[j] + a * sn[j];
+                }
+            }
+            O* dst = kind == 0 ? static_cast<O*>(P.q_out) + ((int64_t)t * P.nH + h) * P.hd
+                               : static_cast<O*>(kind == 1 ? P.kc : P.vc) + (slot * P.nKv + (kind == 1 ? h - P.nH : h - P.nH - P.nKv)) * P.hd;
+            store8(dst + e, x1);
+            store8(dst + e + half, x2);
+        }
     }
 }
 
 template <typename X, typename O>
 cudaError_t launch(const NormRopeParams& P, cudaStream_t s) {
-    return launch_pdl(norm_rope_kernel<X, O>, dim3((P.T + P.tokens - 1) / P.tokens), dim3(kThreads),
-                      (size_t)P.tokens * (P.hd / 2) * sizeof(float2), s, P);
+    const int64_t warps = (int64_t)P.T * P.split;
+    return launch_pdl(norm_rope_kernel<X, O>, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0, s, P);
 }
 template <typename X>
 cudaError_t launch_x(const NormRopeParams& P, int dtype, cudaStream_t s) {
@@ -202,7 +227,9 @@ extern "C" int dspark_norm_rope_paged(const dspark_paged_cache* c, int32_t layer
     P.T = T; P.nH = n_heads; P.nKv = c->n_kv; P.hd = c->head_dim; P.v_norm = v_norm != 0; P.eps = eps;
     P.lanes = 1;
     while (P.lanes * 16 < P.hd) P.lanes *= 2;
-    P.tokens = 1;
+    // few tokens: a token's heads over several warps, until the SMs have a block each or a warp has one round
+    P.split = 1;
+    while ((int64_t)T * P.split < 148 * 8 && P.split * (32 / P.lanes) < n_heads + 2 * c->n_kv) P.split *= 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = x_dtype == DSPARK_DTYPE_F32 ? launch_x<float>(P, c->dtype, s)
                   : x_dtype == DSPARK_DTYPE_F16 ? launch_x<__half>(P, c->dtype, s)

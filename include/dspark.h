@@ -445,7 +445,7 @@ int dspark_page_slots(const dspark_paged_cache* cache, const int32_t* ctx_len, c
  * The rotation turns lane i with lane i + head_dim / 2 by positions[t] *
  * inv_freq[i] (rotate-half, as the draft's own heads; 0 = identity lane); the
  * angle is formed in 64 bits. A token whose slot is negative is padding: nothing
- * is read or written for it. A slot past num_pages * page_size is skipped
+ * is written for it. A slot past num_pages * page_size is skipped
  * likewise and sets DSPARK_DEV_CAPACITY. Two tokens of one call must not share
  * a slot (either's row may remain).
  *   q  device X [T][n_heads][head_dim], k, v device X [T][n_kv][head_dim], X = x_dtype, with
