@@ -40,12 +40,12 @@ namespace {
 
 constexpr int NT = 512;                              // threads; two CTAs an SM
 constexpr int kWarps = NT / 32;
-constexpr int kBins = 1024;
+constexpr int kBins = 2048;
 constexpr int kList = 4096;
 constexpr int kMaxCluster = 16;
 constexpr float kPerUnit = 64.f;                     // bins per unit of (m - x) / T
 constexpr size_t kHeadBytes = kList * 8;             // the histogram, later the list
-constexpr double kSlack = 3e-5;                      // above the relative rounding of a bin and its edge's weight (32 bits, (m - x) / T up to 16)
+constexpr double kSlack = 3e-5;                      // above the relative rounding of a bin and its edge's weight (32 bits, (m - x) / T up to 32)
 constexpr double kFixed = 2251799813685248.0;        // 2^51: sums of kList weights (at most 1) in 63 bits
 
 struct SampleParams {
@@ -58,7 +58,7 @@ struct SampleParams {
 struct Exchange {
     uint64_t best[kMaxCluster];
     double total[kMaxCluster], above[kMaxCluster], kept[kMaxCluster];
-    double lo[kMaxCluster], up[kMaxCluster], cnt[kMaxCluster], listed[kMaxCluster];
+    double share[kMaxCluster], cnt[kMaxCluster], listed[kMaxCluster], first_above[kMaxCluster];
     double bis_mass[2][kMaxCluster], bis_cnt[2][kMaxCluster];
     uint64_t cut;
     unsigned long long piece[kWarps];                // listed entries that stay, per warp's piece of the slice, in 1 / kFixed
@@ -70,7 +70,7 @@ struct Scratch {
     double red[kWarps];
     double wsum[kWarps];
     uint64_t red64[kWarps];
-    double cross_before;
+    double cross_before, cross_upto;
     int cross_bin;
     int found;
 };
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         sort_falling(list, NT);
         bound = key_value((uint32_t)(list[k - 1] >> 32));
         share = key_value((uint32_t)(list[(k - 1) / C] >> 32));
-        tell(S.x.lo, (double)share);
+        tell(S.x.share, (double)share);
     }
     tell(S.x.best, ((uint64_t)__float_as_uint(bound) << 32) | __float_as_uint(mx));
     meet();
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         bound = fmaxf(bound, __uint_as_float((uint32_t)(S.x.best[q] >> 32)));
     }
     if (has_k && !alone && k <= NT) {
-        for (int q = 0; q < C; ++q) share = fminf(share, (float)S.x.lo[q]);
+        for (int q = 0; q < C; ++q) share = fminf(share, (float)S.x.share[q]);
         bound = fmaxf(bound, share);
     }
     // f(x, index) for the entries >= thr (no NaN); threads and vectors without one are skipped
@@ -506,7 +506,6 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         auto upper = [&](int b, uint32_t n, float mean) {     // (the last bin has no end)
             return (double)n * (1.0 + kSlack) * 1.000031 * __expf(-((float)b + (b == kBins - 1 ? 0.f : mean)) * (1.f / kPerUnit));
         };
-        double n = 0.0, lo = 0.0, up = 0.0;
         for (int b = rank * nb + tid; b < (rank + 1) * nb; b += NT) {
             uint32_t c = 0;
             double at = 0.0;
@@ -514,77 +513,82 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
                 c += get_u32(&hist[b], q);
                 at += get_u32(&place[b], q);
             }
-            const float mean = c > 0 ? (float)(at / (1024.0 * c)) : 0.f;
             hist[b] = c;                                      // no other rank reads this rank's share before the next meeting
-            place[b] = __float_as_uint(mean);
-            n += c;
-            lo += lower(b, c, mean);
-            up += upper(b, c, mean);
+            place[b] = __float_as_uint(c > 0 ? (float)(at / (1024.0 * c)) : 0.f);
         }
-        n = block_sum(n, S.red);
-        lo = block_sum(lo, S.red);
-        up = block_sum(up, S.red);
-        tell(S.x.cnt, n);
-        tell(S.x.lo, lo);
-        tell(S.x.up, up);
         meet();
-        // The first bin at which the running sum of `slots` (bins' measure) reaches the
-        // target, or the last of theirs; *before: elements of the bins before it, *upto: with its own.
-        auto cross = [&](const double* slots, auto measure, double* before, double* upto) {
-            double sum = 0.0, cnt = 0.0;
-            int q = 0;
-            for (; q < C - 1 && !(sum + slots[q] >= target); ++q) { sum += slots[q]; cnt += S.x.cnt[q]; }
-            const int per = (nb + NT - 1) / NT;
-            uint32_t c[kBins / NT];
-            double vi[kBins / NT], n = 0.0, v = 0.0;
+        constexpr int PER = kBins / NT;                       // every CTA has all bins, a few a thread
+        uint32_t c[PER];
+        float mean[PER];
 #pragma unroll
-            for (int i = 0; i < kBins / NT; ++i) {
-                const int b = tid * per + i;
-                const bool in = i < per && b < nb;
-                c[i] = in ? get_u32(&hist[q * nb + b], q) : 0u;
-                vi[i] = in ? measure(q * nb + b, c[i], __uint_as_float(get_u32(&place[q * nb + b], q))) : 0.0;
+        for (int i = 0; i < PER; ++i) {
+            const int b = tid * PER + i;
+            c[i] = get_u32(&hist[b], b / nb);
+            mean[i] = __uint_as_float(get_u32(&place[b], b / nb));
+        }
+        // The first bin, from `from` on, at which the running sum of `measure`, `above` to start with, reaches the
+        // target, or the last; *before: elements of the bins before it, *upto: with its own.
+        auto cross = [&](auto measure, int from, double above, double* before, double* upto) {
+            double v[PER], n = 0.0, sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int b = tid * PER + i;
+                v[i] = b >= from ? measure(b, c[i], mean[i]) : 0.0;
+                sum += v[i];
                 n += c[i];
-                v += vi[i];
             }
             double all_v, all_n;
-            double pv = sum + block_scan(v, S.red, &all_v), pn = cnt + block_scan(n, S.red, &all_n);
-            if (tid == 0) S.cross_bin = kBins;
+            double pv = above + block_scan(sum, S.red, &all_v), pn = block_scan(n, S.red, &all_n);
+            if (tid == 0) S.cross_bin = kBins - 1;
             __syncthreads();
-            int mine = kBins;
-            double mine_n = 0.0, mine_c = 0.0;
+            double at = pv;
 #pragma unroll
-            for (int i = 0; i < kBins / NT; ++i) {
-                const int b = tid * per + i;
-                if (i >= per || b >= nb) break;
-                pv += vi[i];
-                if (mine == kBins && pv >= target) { mine = q * nb + b; mine_n = pn; mine_c = c[i]; }
-                pn += c[i];
+            for (int i = 0; i < PER; ++i) {
+                at += v[i];
+                if (tid * PER + i >= from && at >= target) { atomicMin(&S.cross_bin, tid * PER + i); break; }
             }
-            if (mine < kBins) atomicMin(&S.cross_bin, mine);
             __syncthreads();
             const int bin = S.cross_bin;
-            if (mine == bin && mine < kBins) { S.cross_before = mine_n; S.red[0] = mine_n + mine_c; }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (tid * PER + i == bin) { S.cross_before = pn; S.cross_upto = pn + c[i]; }
+                pn += c[i];
+            }
             __syncthreads();
-            *before = bin < kBins ? S.cross_before : cnt;     // (not reached in these bins: their last)
-            *upto = bin < kBins ? S.red[0] : cnt + all_n;
+            *before = S.cross_before;
+            *upto = S.cross_upto;
             __syncthreads();
-            return bin < kBins ? bin : (q + 1) * nb - 1;
+            return bin;
         };
         double before, upto, skip;
-        const int b_lo = cross(S.x.lo, lower, &before, &upto);
+        int b_lo = cross(lower, 0, 0.0, &before, &upto);
         if (upto <= (double)kList) {
             meet();                                           // every rank has read the bins that the list overwrites
             gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { return W.bin(x) <= b_lo; });
             if (rank == 0) finish((int)upto, total);
             return;
         }
-        const int b_up = cross(S.x.up, upper, &before, &skip);
+        int b_up = cross(upper, 0, 0.0, &before, &skip);
+        // The exact mass of bins [from, to) (an x >= sure is in a bin before `to` for sure: most need no bin).
+        auto mass_between = [&](int from, int to) {
+            if (to <= from) return 0.0;
+            const float sure = mx - T * ((float)to * (0.99998f / kPerUnit)) + 1e-6f * fabsf(mx);
+            return from == 0 ? mass_of(edge_x(to - 1), [&](float x, int, double) { return x >= sure || W.bin(x) < to; })
+                             : mass_of(edge_x(to - 1), [&](float x, int, double) { const int b = W.bin(x); return b >= from && b < to; });
+        };
+        // The mass above those bins stays, so without min_p it also is the start of the pieces' kept mass.
+        double mass = mass_between(0, b_up);
+        if (upto - before > (double)kList) {                  // far down the tail the bounds of the whole are too wide: again from the exact mass
+            tell(S.x.first_above, block_sum(mass, S.red));
+            meet();
+            const double above = sum_of(S.x.first_above);
+            const int from = b_up;
+            b_lo = cross(lower, from, above, &skip, &upto);
+            b_up = cross(upper, from, above, &before, &skip);
+            mass += mass_between(from, b_up);
+        }
         if (upto - before <= (double)kList) {
             meet();
-            // The mass above those bins (an x >= sure is in a bin above for sure: most need no bin); it stays,
-            // so without min_p it also is the start of the pieces' kept mass.
-            const float sure = mx - T * ((float)b_up * (0.99998f / kPerUnit)) + 1e-6f * fabsf(mx);
-            const double mass = b_up == 0 ? 0.0 : mass_of(edge_x(b_up - 1), [&](float x, int, double) { return x >= sure || W.bin(x) < b_up; });
             tell(S.x.above, piece_sums(mass));
             const int n = (int)gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { const int b = W.bin(x); return b >= b_up && b <= b_lo; });
             if (rank == 0) {
