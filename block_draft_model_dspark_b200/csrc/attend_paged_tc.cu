@@ -351,9 +351,13 @@ template <> __host__ __device__ constexpr uint32_t idesc<__nv_bfloat16>(int M, i
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int HD_, int NQ_, int KT_, bool QTMEM_>
+template <int HD_, int NQ_, int KT_, bool QTMEM_, bool P16_ = false>
 struct Cfg {
     static constexpr int HD = HD_, NQ = NQ_, KT = KT_;
+    // Pages of 16 rows, one query tile: a page is one copy of all its chunks, [page][chunk][16 rows x 128 B] (a copy a chunk
+    // is 2 KB, and their number then bounds the loads: 990 us for 64 long requests, against 750 with pages of 64). The
+    // MMAs take eight rows at a fixed stride, so the keys go in two classes, rows 0 - 7 of every page, then rows 8 - 15.
+    static constexpr bool P16 = P16_;
     static constexpr bool QTMEM = QTMEM_;                     // Q in tensor memory (staged through ring slots)
     static constexpr int NCH = HD / 64;                       // 64-dimension chunks
     static constexpr int kChunk = kRows * 128;                // a chunk of a query tile
@@ -439,7 +443,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         const int box = min(P.a.page_size, KT), per_tile = KT / box;
-        const int sub = lane / NCH, ch = lane % NCH;          // this lane's request of a tile: box `sub`, chunk `ch`
+        const int sub = C::P16 ? lane : lane / NCH, ch = C::P16 ? 0 : lane % NCH;      // this lane's request of a tile: box `sub`, chunk `ch`
         auto acquire = [&](int entry) {                       // the slot's previous tile has been read
             const int s = entry % NS;
             if (entry >= NS && !__all_sync(0xffffffffu, mbar_wait(&B.free_[s], (uint32_t)(entry / NS - 1) & 1u, abort_flag, P.status)))
@@ -490,14 +494,15 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 const unsigned act = __ballot_sync(0xffffffffu, page != -2);
                 const int k0 = (p.t0 + t) * KT;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&B.full[s], (uint32_t)__popc(act) * (uint32_t)(box * 128));
+                    mbar_arrive_expect_tx(&B.full[s], (uint32_t)__popc(act) * (uint32_t)(box * 128 * (C::P16 ? NCH : 1)));
                     if (v && (k0 < p.lo || k0 + KT > p.hi)) mbar_arrive(&B.vissued[s]);
                 }
                 __syncwarp();
                 if (page != -2) {
                     const int key = k0 + sub * box;
-                    tma_load_2d(ring + (size_t)s * C::kTile + ch * (KT * 128) + sub * (box * 128), m, &B.full[s], p.g * HD + ch * 64,
-                                page * P.a.page_size + (key & (P.a.page_size - 1)));
+                    const int row = page * P.a.page_size + (key & (P.a.page_size - 1));
+                    if (C::P16) tma_load_3d(ring + (size_t)s * C::kTile + sub * (NCH * 2048), m, &B.full[s], 0, row, p.g * NCH);
+                    else tma_load_2d(ring + (size_t)s * C::kTile + ch * (KT * 128) + sub * (box * 128), m, &B.full[s], p.g * HD + ch * 64, row);
                 }
                 ++e;
                 issued = e;
@@ -526,7 +531,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         // The whole warp runs the loop, so that what an MMA takes (descriptors, addresses) stays in uniform
         // registers; one elected thread issues.
         uint32_t vpar = 0;                                    // parity of each slot's next vready phase
-        constexpr uint32_t id_qk = idesc<T>(kRows, KT, 0), id_pv = idesc<T>(kRows, HD, 1);
+        constexpr uint32_t id_qk = idesc<T>(kRows, C::P16 ? KT / 2 : KT, 0), id_pv = idesc<T>(kRows, HD, 1);
         const bool leader = elect_one();
         const uint32_t ring0 = smem_u32(ring), q0 = smem_u32(sQ);
         auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, P.status); };
@@ -543,16 +548,17 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 tc_fence_after();
                 if (leader) {
                     const uint32_t d = tmem + (uint32_t)(buf * KT);
-                    const uint64_t bd = sdesc_k_sw128(ring0 + (uint32_t)sl * C::kTile);
-                    if (C::QTMEM) {
+                    constexpr int kChunkB = C::P16 ? 2048 : KT * 128;       // bytes between chunks of K
 #pragma unroll
-                        for (int j = 0; j < HD / 16; ++j)
-                            mma_f16_ts(d, tmem + (uint32_t)(C::kQCol + 8 * j), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
-                    } else {
+                    for (int h = 0; h < (C::P16 ? 2 : 1); ++h) {
+                        const uint64_t bd = sdesc_k_sw128(ring0 + (uint32_t)sl * C::kTile + h * 1024, C::P16 ? NCH * 2048 : 1024);
                         const uint64_t ad = sdesc_k_sw128(q0 + (uint32_t)(q * NCH * C::kChunk));
 #pragma unroll
-                        for (int j = 0; j < HD / 16; ++j)
-                            mma_bf16(d, ad + (uint64_t)(((j >> 2) * C::kChunk + (j & 3) * 32) >> 4), bd + (uint64_t)(((j >> 2) * KT * 128 + (j & 3) * 32) >> 4), id_qk, j > 0);
+                        for (int j = 0; j < HD / 16; ++j) {
+                            const uint64_t bj = bd + (uint64_t)(((j >> 2) * kChunkB + (j & 3) * 32) >> 4);
+                            if (C::QTMEM) mma_f16_ts(d + h * (KT / 2), tmem + (uint32_t)(C::kQCol + 8 * j), bj, id_qk, j > 0);
+                            else mma_bf16(d + h * (KT / 2), ad + (uint64_t)(((j >> 2) * C::kChunk + (j & 3) * 32) >> 4), bj, id_qk, j > 0);
+                        }
                     }
                     mma_commit(&B.sdone[buf]);
                     if (q == NQ - 1) mma_commit(&B.free_[sl]);
@@ -572,7 +578,9 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     if (part) vpar ^= 1u << sl;
                 }
                 const uint32_t d = tmem + (uint32_t)(C::kOCol + q * HD), pa = tmem + (uint32_t)(buf * KT);
-                const uint64_t bd = sdesc_mn_sw128(ring0 + (uint32_t)sl * C::kTile, KT * 128);
+                const uint64_t bd = sdesc_mn_sw128(ring0 + (uint32_t)sl * C::kTile, C::P16 ? 2048 : KT * 128, C::P16 ? NCH * 2048 : 1024);
+                // keys 16 j ..: with P16 rows 0 - 7 (then 8 - 15) of two pages
+                auto v_at = [](int j) { return C::P16 ? 2 * (j % (KT / 32)) * NCH * 2048 + j / (KT / 32) * 1024 : j * 2048; };
                 constexpr int J0 = NQ == 2 ? 4 : 0;           // MMAs on the half of P that is ready first
                 if (NQ == 2) {
                     if (!__all_sync(0xffffffffu, wait(&B.phalf[buf], (uint32_t)((g0 + s) >> 1) & 1u))) { ok = false; break; }
@@ -580,7 +588,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     if (leader) {
 #pragma unroll
                         for (int j = 0; j < J0; ++j)
-                            mma_f16_ts(d, pa + (uint32_t)(8 * j), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
+                            mma_f16_ts(d, pa + (uint32_t)(8 * j), bd + (uint64_t)(v_at(j) >> 4), id_pv, t > 0 || j > 0);
                     }
                 }
                 if (!__all_sync(0xffffffffu, wait(&B.pready[buf], (uint32_t)((g0 + s) >> 1) & 1u))) { ok = false; break; }
@@ -588,7 +596,7 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 if (leader) {
 #pragma unroll
                     for (int j = J0; j < KT / 16; ++j)
-                        mma_f16_ts(d, pa + (uint32_t)(j / (C::CH / 16) * C::CH + j % (C::CH / 16) * 8), bd + (uint64_t)((j * 2048) >> 4), id_pv, t > 0 || j > 0);
+                        mma_f16_ts(d, pa + (uint32_t)(j / (C::CH / 16) * C::CH + j % (C::CH / 16) * 8), bd + (uint64_t)(v_at(j) >> 4), id_pv, t > 0 || j > 0);
                     mma_commit(&B.odone[buf]);
                     if (q == NQ - 1) mma_commit(&B.free_[sl]);
                 }
@@ -621,10 +629,10 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 uint8_t* tile = ring + (size_t)sl * C::kTile;
                 const int dead = KT - (b - a);
                 for (int i = lane; i < dead * 8; i += 32) {
-                    const int row = i >> 3;
-                    uint8_t* line = tile + (row < a ? row : row - a + b) * 128 + (i & 7) * 16;
+                    const int row = (i >> 3) < a ? i >> 3 : (i >> 3) - a + b;
+                    uint8_t* line = tile + (C::P16 ? row / 16 * (NCH * 2048) + row % 16 * 128 : row * 128) + (i & 7) * 16;
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) *reinterpret_cast<uint4*>(line + c * (KT * 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int c = 0; c < NCH; ++c) *reinterpret_cast<uint4*>(line + c * (C::P16 ? 2048 : KT * 128)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_shared();                         // the MMAs read through the async proxy
                 __syncwarp();
@@ -709,10 +717,13 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     for (int i = 0; i < W; i += 32) tmem_ld_x32(tS + (uint32_t)(j + i), u + i);
                     tmem_ld_wait();
                     if (edge) {
-                        const int a = row_lo - k0 - half * CH - j, b = row_hi - k0 - half * CH - j;
+                        // column i's key is k0 + first + place(i)
+                        const int first = C::P16 ? half * 8 + 2 * j : half * CH + j, a = row_lo - k0 - first, b = row_hi - k0 - first;
 #pragma unroll
-                        for (int i = 0; i < W; ++i)
-                            if (i < a || i >= b) u[i] = 0xff800000u;
+                        for (int i = 0; i < W; ++i) {
+                            const int place = C::P16 ? i / 8 * 16 + i % 8 : i;
+                            if (place < a || place >= b) u[i] = 0xff800000u;
+                        }
                     }
                 };
 #pragma unroll
@@ -957,11 +968,18 @@ cudaError_t launch(Params P, cudaStream_t s) {
     const cuuint64_t qs[3] = {hb, hb * a.grp, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t qb[4] = {64, (cuuint32_t)a.grp, 1, (cuuint32_t)P.tpt};
     // (a page is page_size rows of all kv heads: the fewer dimensions, the faster small boxes go)
-    const cuuint64_t kd[2] = {(cuuint64_t)a.nKv * a.hd, (cuuint64_t)a.num_pages * a.page_size};
-    const cuuint64_t ks[1] = {hb * a.nKv};
-    const cuuint32_t kb[2] = {64, (cuuint32_t)std::min(a.page_size, C::KT)};
-    if (!make_map(&tq, a.q, a.dtype, qd, qs, qb) || !make_map(&tk, a.k, a.dtype, kd, ks, kb) || !make_map(&tv, a.v, a.dtype, kd, ks, kb))
-        return cudaErrorInvalidValue;
+    const cuuint64_t rows = (cuuint64_t)a.num_pages * a.page_size;
+    bool ok = make_map(&tq, a.q, a.dtype, qd, qs, qb);
+    if (C::P16) {
+        const cuuint64_t kd[3] = {64, rows, (cuuint64_t)a.nKv * C::NCH}, ks[2] = {hb * a.nKv, 128};
+        const cuuint32_t kb[3] = {64, 16, C::NCH};
+        ok = ok && make_map(&tk, a.k, a.dtype, kd, ks, kb) && make_map(&tv, a.v, a.dtype, kd, ks, kb);
+    } else {
+        const cuuint64_t kd[2] = {(cuuint64_t)a.nKv * a.hd, rows}, ks[1] = {hb * a.nKv};
+        const cuuint32_t kb[2] = {64, (cuuint32_t)std::min(a.page_size, C::KT)};
+        ok = ok && make_map(&tk, a.k, a.dtype, kd, ks, kb) && make_map(&tv, a.v, a.dtype, kd, ks, kb);
+    }
+    if (!ok) return cudaErrorInvalidValue;
     auto kern = attend_paged_tc_kernel<T, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
@@ -976,11 +994,12 @@ cudaError_t dispatch(const Params& P, cudaStream_t s) {
     // two query tiles per unit once a request's rows fill more than one: K and V tiles then feed twice the
     // MMAs and the softmax of one tile overlaps the MMAs of the other
     const bool two = (int64_t)P.a.max_new * P.a.grp > kRows;
+    const bool p16 = P.a.page_size == 16;
     switch (P.a.hd) {
-        case 64: return two ? launch<T, Cfg<64, 2, 128, false>>(P, s) : launch<T, Cfg<64, 1, 128, false>>(P, s);
-        case 128: return two ? launch<T, Cfg<128, 2, 128, false>>(P, s) : launch<T, Cfg<128, 1, 128, false>>(P, s);
-        case 192: return launch<T, Cfg<192, 1, 64, true>>(P, s);
-        default: return launch<T, Cfg<256, 1, 64, true>>(P, s);
+        case 64: return two ? launch<T, Cfg<64, 2, 128, false>>(P, s) : p16 ? launch<T, Cfg<64, 1, 128, false, true>>(P, s) : launch<T, Cfg<64, 1, 128, false>>(P, s);
+        case 128: return two ? launch<T, Cfg<128, 2, 128, false>>(P, s) : p16 ? launch<T, Cfg<128, 1, 128, false, true>>(P, s) : launch<T, Cfg<128, 1, 128, false>>(P, s);
+        case 192: return p16 ? launch<T, Cfg<192, 1, 64, true, true>>(P, s) : launch<T, Cfg<192, 1, 64, true>>(P, s);
+        default: return p16 ? launch<T, Cfg<256, 1, 64, true, true>>(P, s) : launch<T, Cfg<256, 1, 64, true>>(P, s);
     }
 }
 
