@@ -31,6 +31,7 @@
 // 2^-46: 12 64-bit operations an element.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "paged.h"
 #include "tc_ptx.cuh"
@@ -207,19 +208,24 @@ __device__ void sort_falling(uint64_t* a, int n) {
 // Adds the weights of a vector's entries >= thr that `pred` accepts; no branches, so that their 64-bit chains overlap.
 template <int VEC, typename Pred>
 __device__ __forceinline__ void add_mass(const Weights& W, const float (&x)[VEC], int i0, float thr, Pred pred, double& a, double& b) {
-    double w[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = W.raw(x[i]);
+    for (int h = 0; h < VEC; h += 4) {                        // (four chains: eight do not fit the registers)
+        double w[4];
 #pragma unroll
-    for (int i = 0; i < VEC; i += 2) {
-        if (x[i] >= thr && pred(x[i], i0 + i, w[i])) a += w[i];
-        if (x[i + 1] >= thr && pred(x[i + 1], i0 + i + 1, w[i + 1])) b += w[i + 1];
+        for (int i = 0; i < 4; ++i) w[i] = W.raw(x[h + i]);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            if (x[h + i] >= thr && pred(x[h + i], i0 + h + i, w[i])) a += w[i];
+            if (x[h + i + 1] >= thr && pred(x[h + i + 1], i0 + h + i + 1, w[i + 1])) b += w[i + 1];
+        }
     }
 }
 
 template <typename X>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
-    constexpr int VEC = 16 / (int)sizeof(X), BATCH = 4;       // vectors in flight a thread
+    constexpr int VEC = 16 / (int)sizeof(X);
+    using Light = std::integral_constant<int, 6>;             // vectors in flight a thread: passes that only compare,
+    using Heavy = std::integral_constant<int, 2>;             // and those that sum weights
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);       // [kBins] elements
     uint32_t* place = hist + kBins;                           // [kBins] their places in the bin, in 1/1024; then the mean as a float
@@ -268,7 +274,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         return !inf_max ? x : x == INFINITY ? 0.f : -INFINITY;
     };
     // f(x[VEC], index of the first, their maximum (a NaN loses)) over vectors [a, b) of the slice, `step` apart
-    auto scan = [&](int a, int b, int step, bool first, auto f) {
+    auto scan = [&](auto batch, int a, int b, int step, bool first, auto f) {
+        constexpr int BATCH = decltype(batch)::value;
         for (int v = a; v < b; v += BATCH * step) {
             uint4 raw[BATCH];
 #pragma unroll
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
             }
         }
     };
-    auto each = [&](auto f) { scan(v0 + lane, v1, 32, false, f); };      // over the slice, a contiguous piece per warp
+    auto each = [&](auto batch, auto f) { scan(batch, v0 + lane, v1, 32, false, f); };      // over the slice, a contiguous piece per warp
     auto meet = [&] { if (C > 1) cluster_sync(); else __syncthreads(); };
     auto tell = [&](auto* slots, auto v) { if (tid < C) put(&slots[rank], tid, v); };   // this rank's number, to every CTA
     auto sum_of = [&](const double* slots) {
@@ -299,9 +306,22 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     // ---------------------------------------------------------------- the maximum, and the mass
     float best = -INFINITY;
     double sum0 = 0.0, sum1 = 0.0;
-    if (sum_now) {
+    if (sum_now && !P.resident) {
         W.at(best);
-        scan(v0 + lane, v1, 32, true, [&](const float (&x)[VEC], int i0, float hi) {
+        constexpr int B = Heavy::value;
+        for (int v = v0 + lane; v < v1; v += B * 32) {
+            uint4 raw[B];
+            float hi = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < B; ++q)
+                if (v + 32 * q < v1) raw[q] = fetch(v + 32 * q);
+#pragma unroll
+            for (int q = 0; q < B; ++q) {
+                if (v + 32 * q >= v1) break;
+                const X* e = reinterpret_cast<const X*>(&raw[q]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) hi = fmaxf(hi, to_f(e[i]));      // (a NaN loses)
+            }
             if (hi > best) {                                  // the sums so far, relative to the new maximum
                 W.at(hi);
                 const double f = W(best);
@@ -309,10 +329,18 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
                 sum1 *= f;
                 best = hi;
             }
-            add_mass<VEC>(W, x, i0, W.cutoff, any, sum0, sum1);
-        });
+#pragma unroll
+            for (int q = 0; q < B; ++q) {
+                if (v + 32 * q >= v1) break;
+                const X* e = reinterpret_cast<const X*>(&raw[q]);
+                float x[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) x[i] = to_f(e[i]);
+                add_mass<VEC>(W, x, 0, W.cutoff, any, sum0, sum1);
+            }
+        }
     } else {
-        scan(v0 + lane, v1, 32, true, [&](const float (&)[VEC], int, float hi) { best = fmaxf(best, hi); });
+        scan(Light{}, v0 + lane, v1, 32, true, [&](const float (&)[VEC], int, float hi) { best = fmaxf(best, hi); });
     }
     float mx = block_reduce(best, reinterpret_cast<float*>(S.red64), [](float x, float y) { return fmaxf(x, y); });
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -339,7 +367,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     // f(x, index) for the entries >= thr (no NaN); threads and vectors without one are skipped
     auto each_from = [&](float thr, auto f) {
         if (!(best >= thr)) return;
-        each([&](const float (&x)[VEC], int i0, float hi) {
+        each(Light{}, [&](const float (&x)[VEC], int i0, float hi) {
             if (hi >= thr) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
@@ -351,7 +379,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         double a = 0.0, b = 0.0;
         thr = fmaxf(thr, W.cutoff);
         if (best >= thr)
-            each([&](const float (&x)[VEC], int i0, float hi) { if (hi >= thr) add_mass<VEC>(W, x, i0, thr, pred, a, b); });
+            each(Heavy{}, [&](const float (&x)[VEC], int i0, float hi) { if (hi >= thr) add_mass<VEC>(W, x, i0, thr, pred, a, b); });
         return a + b;
     };
     auto largest_alone = [&] {                                 // the lowest index of the maximum
@@ -388,7 +416,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         if (sum_now) mine = mass_of(-FLT_MAX, any);
     } else {
         W.at(mx);
-        if (sum_now) mine = (sum0 + sum1) * W(best);
+        if (sum_now) mine = P.resident ? mass_of(-FLT_MAX, any) : (sum0 + sum1) * W(best);
     }
 
     uint64_t cut = 0;                                         // candidates below it are dropped
@@ -715,7 +743,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     const int a0 = min(nvec, piece * per_warp), a1 = min(nvec, a0 + per_warp), each_n = (a1 - a0 + NT - 1) / NT;
     const int t0 = min(a1, a0 + tid * each_n), t1 = min(a1, t0 + each_n);
     auto piece_scan = [&](auto f) {
-        scan(t0, t1, 1, false, [&](const float (&x)[VEC], int i0, float hi) {
+        scan(Heavy{}, t0, t1, 1, false, [&](const float (&x)[VEC], int i0, float hi) {
             if (!(hi >= thr)) return;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -754,7 +782,7 @@ cudaError_t launch(SampleParams P, cudaStream_t s) {
     auto slice = [&](int c) { return (int)(((int64_t)P.V + VEC - 1 + c - 1) / c + VEC - 1) / VEC * VEC; };
     // Rows are split while they leave SMs idle (148, two CTAs each) and a slice is long enough to pay for the exchanges.
     int c = 1;
-    while (c < kMaxCluster && (int64_t)P.rows * c * 2 <= 320 && slice(c) > 4096) c *= 2;
+    while (c < kMaxCluster && (int64_t)P.rows * c * 2 <= 296 && slice(c) > 4096) c *= 2;
     P.cluster = c;
     P.slice = slice(c);
     // Shared memory for two CTAs an SM, or for one where there are no more CTAs than SMs.
