@@ -432,18 +432,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         for (int w = 0; w < kWarps; ++w) t += S.wsum[w];
         return t;
     };
-    // The chosen entries' ranks into the list of CTA 0; how many there are.
-    auto gather = [&](float thr, auto chosen) {
-        int n = 0;
-        each_from(thr, [&](float x, int i) {
-            if (!chosen(x)) return;
-            ++n;
-            const uint32_t at = C > 1 ? add_u32(&S.x.n_list, 0, 1u) : atomicAdd(&S.x.n_list, 1u);
-            if (at < (uint32_t)kList) {
-                if (C > 1) put(&list[at], 0, rank_of(x, i)); else list[at] = rank_of(x, i);
-            }
-        });
-        tell(S.x.listed, (double)block_reduce(n, reinterpret_cast<int*>(S.red64), [](int a, int b) { return a + b; }));
+    // An entry's rank into the list of CTA 0; how many there are in all.
+    int listed = 0;
+    auto push = [&](float x, int i) {
+        ++listed;
+        const uint32_t at = C > 1 ? add_u32(&S.x.n_list, 0, 1u) : atomicAdd(&S.x.n_list, 1u);
+        if (at < (uint32_t)kList) {
+            if (C > 1) put(&list[at], 0, rank_of(x, i)); else list[at] = rank_of(x, i);
+        }
+    };
+    auto count_list = [&] {
+        tell(S.x.listed, (double)block_reduce(listed, reinterpret_cast<int*>(S.red64), [](int a, int b) { return a + b; }));
         meet();
         return sum_of(S.x.listed);
     };
@@ -502,7 +501,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     if (has_k) {
         bisect = true;
         if (bound > -INFINITY) {
-            const double n = gather(bound, [](float) { return true; });
+            each_from(bound, push);
+            const double n = count_list();
             if (n <= (double)kList) {
                 if (rank == 0) finish((int)n, 0.0);
                 return;
@@ -592,33 +592,37 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         int b_lo = cross(lower, 0, 0.0, &before, &upto);
         if (upto <= (double)kList) {
             meet();                                           // every rank has read the bins that the list overwrites
-            gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { return W.bin(x) <= b_lo; });
+            each_from(fmaxf(bound, edge_x(b_lo)), [&](float x, int i) { if (W.bin(x) <= b_lo) push(x, i); });
+            count_list();
             if (rank == 0) finish((int)upto, total);
             return;
         }
         int b_up = cross(upper, 0, 0.0, &before, &skip);
-        // The exact mass of bins [from, to) (an x >= sure is in a bin before `to` for sure: most need no bin).
-        auto mass_between = [&](int from, int to) {
-            if (to <= from) return 0.0;
-            const float sure = mx - T * ((float)to * (0.99998f / kPerUnit)) + 1e-6f * fabsf(mx);
-            return from == 0 ? mass_of(edge_x(to - 1), [&](float x, int, double) { return x >= sure || W.bin(x) < to; })
-                             : mass_of(edge_x(to - 1), [&](float x, int, double) { const int b = W.bin(x); return b >= from && b < to; });
-        };
         // The mass above those bins stays, so without min_p it also is the start of the pieces' kept mass.
-        double mass = mass_between(0, b_up);
-        if (upto - before > (double)kList) {                  // far down the tail the bounds of the whole are too wide: again from the exact mass
+        double mass = 0.0;
+        int from = 0;
+        if (upto - before > (double)kList && b_up > 0) {      // far down the tail the bounds of the whole are too wide: again from the exact mass
+            from = b_up;
+            mass = mass_of(edge_x(from - 1), [&](float x, int, double) { return W.bin(x) < from; });
             tell(S.x.first_above, block_sum(mass, S.red));
             meet();
             const double above = sum_of(S.x.first_above);
-            const int from = b_up;
             b_lo = cross(lower, from, above, &skip, &upto);
             b_up = cross(upper, from, above, &before, &skip);
-            mass += mass_between(from, b_up);
         }
         if (upto - before <= (double)kList) {
             meet();
+            // one pass for the exact mass of bins [from, b_up) and the list of bins [b_up, b_lo] (an x >= sure is above them
+            // for sure: most need no bin)
+            const float sure = from > 0 ? INFINITY : mx - T * ((float)b_up * (0.99998f / kPerUnit)) + 1e-6f * fabsf(mx);
+            mass += mass_of(fmaxf(bound, edge_x(b_lo)), [&](float x, int i, double) {
+                if (x >= sure && b_up > 0) return true;
+                const int b = W.bin(x);
+                if (b >= b_up && b <= b_lo) push(x, i);
+                return b >= from && b < b_up;
+            });
             tell(S.x.above, piece_sums(mass));
-            const int n = (int)gather(fmaxf(bound, edge_x(b_lo)), [&](float x) { const int b = W.bin(x); return b >= b_up && b <= b_lo; });
+            const int n = (int)count_list();
             if (rank == 0) {
                 const int per = (sort_list(n) + NT - 1) / NT;
                 double own = 0.0, all;
