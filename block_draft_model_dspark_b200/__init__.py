@@ -364,13 +364,14 @@ def page_slots(cache: PagedKvCache, ctx_len, n_new, n_pages, free_pages, free_co
     return cu_new, kv_len, slots, positions, n_pages_out, free_count_out
 
 
-def _heads(t, name: str, n_heads: Optional[int], hd: int, dev: int):
-    """Checks [T, heads, hd] with contiguous heads on the device; returns the token stride."""
-    if t.dim() != 3 or t.shape[2] != hd or (n_heads is not None and t.shape[1] != n_heads) or t.get_device() != dev or \
-            t.stride(2) != 1 or (t.stride(1) != hd and t.shape[1] > 1):
-        _refuse(f"{name} must be [T, heads, {hd}] on cuda:{dev} with contiguous heads" +
-                (f" ({n_heads} of them)" if n_heads is not None else ""))
-    return t.stride(0)
+def _heads(t, name: str, shape, n_heads: Optional[int], hd: int, dev: int):
+    """Checks [T, heads, hd] (its shape given) with contiguous heads on the device; returns the token stride."""
+    if len(shape) == 3 and shape[2] == hd and (n_heads is None or shape[1] == n_heads) and t.get_device() == dev:
+        st = t.stride()
+        if st[2] == 1 and (st[1] == hd or shape[1] <= 1):
+            return st[0]
+    _refuse(f"{name} must be [T, heads, {hd}] on cuda:{dev} with contiguous heads" +
+            (f" ({n_heads} of them)" if n_heads is not None else ""))
 
 
 def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: PagedKvCache, layer: int, eps: float = 1e-6,
@@ -381,15 +382,20 @@ def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: 
     ``rope_inv_freq``); ``positions`` int32 [T], ``slots`` int64 [T] (negative: a padding row, left alone).
     Returns q_out [T, nH, hd] in the cache's dtype."""
     import torch
-    hd, dev, T, nH = cache.head_dim, cache.dev, q.shape[0], q.shape[1]
-    qs, ks = _heads(q, "q", None, hd, dev), _heads(k, "k", cache.n_kv, hd, dev)
-    vs = _heads(v, "v", cache.n_kv, hd, dev) if v is not None else 0
-    dt = q.dtype
-    if k.dtype is not dt or k.shape[0] < T or (v is not None and (v.dtype is not dt or v.shape[0] < T)):
+    hd, dev, n_kv = cache.head_dim, cache.dev, cache.n_kv
+    q_shape, k_shape, dt = q.shape, k.shape, q.dtype
+    qs, ks, vs = _heads(q, "q", q_shape, None, hd, dev), _heads(k, "k", k_shape, n_kv, hd, dev), 0
+    T, nH = q_shape[0], q_shape[1]
+    if k.dtype is not dt or k_shape[0] < T:
         _refuse("q, k and v must have one dtype and the same tokens")
+    if v is not None:
+        v_shape = v.shape
+        vs = _heads(v, "v", v_shape, n_kv, hd, dev)
+        if v.dtype is not dt or v_shape[0] < T:
+            _refuse("q, k and v must have one dtype and the same tokens")
     if q_out is None:
         q_out = _empty((T, nH, hd), cache.dtype, cache.device, stream)
-    elif q_out.dtype is not cache.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != dev:
+    elif q_out.dtype is not cache.dtype or q_out.shape != q_shape or not q_out.is_contiguous() or q_out.get_device() != dev:
         _refuse("q_out must be a contiguous [T, heads, head_dim] tensor in the cache's dtype")
     _launch(get_lib().dspark_norm_rope_paged, dev, stream,
             cache.ref, layer, _dtype_code(dt), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, nH,
@@ -425,18 +431,17 @@ def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: in
     gives them, ``max_new`` the most new tokens of a request. Returns out [T, nH, hd]; ``lse`` float32
     [T, nH] is filled if given."""
     import torch
-    if q.dim() != 3 or kv_len.dim() != 1:
-        _refuse("q must be [T, heads, head_dim] and kv_len one-dimensional")
-    (T, nH, _), dev, B = q.shape, cache.dev, kv_len.shape[0]
-    qs = _heads(q, "q", None, cache.head_dim, dev)
-    if q.dtype is not cache.dtype:
-        _refuse("q must be in the cache's dtype")
+    shape, hd, dev = q.shape, cache.head_dim, cache.dev
+    qs = _heads(q, "q", shape, None, hd, dev)
+    if q.dtype is not cache.dtype or kv_len.dim() != 1:
+        _refuse("q must be in the cache's dtype and kv_len one-dimensional")
+    T, nH, B = shape[0], shape[1], kv_len.numel()
     if out is None:
-        out = _empty((T, nH, cache.head_dim), cache.dtype, cache.device, stream)
-    elif out.dtype is not cache.dtype or out.shape != q.shape:
+        out = _empty((T, nH, hd), cache.dtype, cache.device, stream)
+    elif out.dtype is not cache.dtype or out.shape != shape:
         _refuse("out must have q's shape and the cache's dtype")
-    os_ = _heads(out, "out", nH, cache.head_dim, dev)
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or
+    os_ = _heads(out, "out", shape, nH, hd, dev)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous() or
                             lse.get_device() != dev):
         _refuse("lse must be a contiguous float32 tensor [T, heads]")
     if ws is None:
