@@ -196,6 +196,7 @@ extern "C" int dspark_page_slots(const dspark_paged_cache* c, const int32_t* ctx
     if (rc != DSPARK_OK) return rc;
     if (B < 1 || B > c->batch) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "B must be in [1, cache.batch]");
     if (B > kMaxBatch) DSPARK_FAIL(DSPARK_ERR_UNSUPPORTED, "more than 4096 requests in one call");
+    if (max_tokens > (1 << 30)) DSPARK_FAIL(DSPARK_ERR_UNSUPPORTED, "max_tokens above 2^30");
     if (max_tokens < 0 || n_free < 0) DSPARK_FAIL(DSPARK_ERR_INVALID_ARGUMENT, "max_tokens and n_free must be >= 0");
     if (!ctx_len || !n_new || !n_pages || !free_count || !n_pages_out || !free_count_out || !cu_new || !kv_len ||
         (n_free > 0 && !free_pages) || (max_tokens > 0 && (!slots || !positions)))

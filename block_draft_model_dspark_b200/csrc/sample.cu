@@ -347,9 +347,20 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     // Lower bounds of the row's k-th largest: the k-th largest of the threads' maxima, of whichever CTA has the highest;
     // and, k / C of the candidates from each CTA, the lowest of their (k / C)-th.
     float bound = -INFINITY, share = -INFINITY;
-    if (has_k && !alone && k <= NT) {
-        list[tid] = (uint64_t)order_key(best) << 32;
-        sort_falling(list, NT);
+    // (more than a thread's maximum each for k > NT: the maxima of eight parts of its vectors)
+    const bool listable = has_k && !alone && k <= kList / 2;
+    if (listable) {
+        const int parts = k <= NT ? 1 : kList / NT;
+        for (int i = tid; i < parts * NT; i += NT) list[i] = (uint64_t)order_key(parts == 1 ? best : -INFINITY) << 32;
+        if (parts > 1) {
+            int part = 0;
+            scan(Light{}, v0 + lane, v1, 32, !P.resident, [&](const float (&)[VEC], int, float hi) {
+                uint64_t& most = list[part * NT + tid];
+                most = max(most, (uint64_t)order_key(hi) << 32);
+                part = part + 1 == parts ? 0 : part + 1;
+            });
+        }
+        sort_falling(list, parts * NT);
         bound = key_value((uint32_t)(list[k - 1] >> 32));
         share = key_value((uint32_t)(list[(k - 1) / C] >> 32));
         tell(S.x.share, (double)share);
@@ -360,7 +371,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         mx = fmaxf(mx, __uint_as_float((uint32_t)S.x.best[q]));
         bound = fmaxf(bound, __uint_as_float((uint32_t)(S.x.best[q] >> 32)));
     }
-    if (has_k && !alone && k <= NT) {
+    if (listable) {
         for (int q = 0; q < C; ++q) share = fminf(share, (float)S.x.share[q]);
         bound = fmaxf(bound, share);
     }

@@ -429,7 +429,7 @@ typedef struct dspark_paged_cache {
  * DSPARK_DEV_CAPACITY in the cache's status: cu_new is then 0 throughout, every
  * slot -1, kv_len = ctx_len, and pages, counts and tables stay as they were. A page number outside
  * [0, num_pages) sets DSPARK_DEV_BAD_PAGE and gives its tokens slot -1. cache.k
- * and cache.v are not read. B <= 4096.
+ * and cache.v are not read. B <= 4096, max_tokens <= 2^30.
  */
 int dspark_page_slots(const dspark_paged_cache* cache, const int32_t* ctx_len, const int32_t* n_new, int32_t B,
                       const int32_t* n_pages, const int32_t* free_pages, int32_t n_free, const int32_t* free_count,
@@ -482,11 +482,11 @@ int dspark_norm_rope_paged(const dspark_paged_cache* cache, int32_t layer, int32
  *        that may overlap on the GPU need one each
  * Scores, softmax and sums are fp32; the probabilities that multiply V are rounded to KV.
  * Cache rows that no query of a request sees are never used, whatever they hold; a row that some query
- * sees must be finite. Lengths past max_pages * page_size are clamped (DSPARK_DEV_BAD_LENGTH); a page
+ * sees must be finite. Lengths past max_pages * page_size or 2^30 are clamped (DSPARK_DEV_BAD_LENGTH); a page
  * outside [0, num_pages) reads as zeros (DSPARK_DEV_BAD_PAGE). A kernel whose copies never arrive
  * gives up (DSPARK_DEV_WAIT_TIMEOUT). bf16 and fp16 caches with head_dim a multiple of 64
  * and page_size a power of two >= 8 run on the tensor cores, others on the CUDA cores. q, out, k
- * and v are 16-byte aligned, the strides multiples of 16 bytes.
+ * and v are 16-byte aligned, the strides multiples of 16 bytes and at least n_heads * head_dim. B <= 4096.
  */
 size_t dspark_attend_paged_workspace_bytes(const dspark_paged_cache* cache, int32_t T, int32_t n_heads, int32_t B);
 int dspark_attend_paged(const dspark_paged_cache* cache, int32_t layer, const void* q, int64_t q_stride,

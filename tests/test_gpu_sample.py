@@ -154,3 +154,13 @@ def test_more_rows_than_sms():
     for n in (1, 7, 60):
         part = dsp.sample(x[:n].cuda(), torch.from_numpy(u[:n]).cuda(), **{k: t[:n].contiguous() for k, t in dev.items()}).cpu()
         assert (part != whole[:n]).sum() <= 0
+
+
+@pytest.mark.parametrize("R", [3, 200])
+def test_top_k_of_every_size(R):
+    """Around the list's sizes: a thread's maximum each (512), eight (2048), and beyond."""
+    x, rng = logits(9, R, 30011, "fp32")
+    u = rng.random(R, dtype=np.float32)
+    for k in (1, 2, 511, 512, 513, 1500, 2047, 2048, 2049, 30010):
+        check(x, u, top_k=np.full(R, k, np.int32))
+    check(x, u, top_k=rng.integers(400, 2300, R).astype(np.int32), top_p=np.full(R, 0.95, np.float32), min_p=np.full(R, 0.001, np.float32))

@@ -79,6 +79,7 @@ def test_page_slots_refusals(dsp):
         refused(dsp, lib.dspark_page_slots(*slots_args(c, **kw)), -1)
     big = cache(dsp, batch=5000)
     refused(dsp, lib.dspark_page_slots(*slots_args(big, B=4097)), -2)
+    refused(dsp, lib.dspark_page_slots(*slots_args(c, max_tokens=(1 << 30) + 1)), -2)
 
 
 def test_norm_rope_refusals(dsp):
@@ -106,6 +107,10 @@ def test_attend_refusals(dsp):
     assert need > 0
     refused(dsp, lib.dspark_attend_paged(*attend_args(c, ws_bytes=need - 1)), -4)
     refused(dsp, lib.dspark_attend_paged(*attend_args(c, T=1 << 30)), -2)
+    for kw in (dict(q_stride=504), dict(out_stride=256)):           # tokens that overlap
+        refused(dsp, lib.dspark_attend_paged(*attend_args(c, **kw)), -1)
+    big = cache(dsp, batch=5000)
+    refused(dsp, lib.dspark_attend_paged(*attend_args(big, B=4097)), -2)
     assert lib.dspark_attend_paged(*attend_args(c, T=0, q=None)) == 0
     assert lib.dspark_attend_paged(*attend_args(c, B=0, kv_len=None)) == 0
 
