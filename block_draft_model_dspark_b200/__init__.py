@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +110,7 @@ _PROTOTYPES = {
     "dspark_sample_workspace_bytes": (c_size, [c_i32, c_i32]),
     "dspark_sample": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
                               c_vp]),
+    "dspark_packed_call": (c_i32, [c_i32, ctypes.c_char_p]),
     "dspark_debug_attention_dump": (c_i32, [c_vp, c_vp, c_size]),
     "dspark_debug_logit_stats": (c_i32, [c_vp, c_vp, c_size]),
     "dspark_debug_wait_probe": (c_i32, [c_vp, c_i32, c_vp]),
@@ -260,6 +262,10 @@ def _refuse(msg: str):
     raise DsparkError(DSPARK_ERR_INVALID_ARGUMENT, msg)
 
 
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
 def _vec(t, name: str, dtype, n: int, dev: int):
     """Checks a contiguous device array of at least n entries; returns its address."""
     if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
@@ -267,17 +273,21 @@ def _vec(t, name: str, dtype, n: int, dev: int):
     _refuse(f"{name} must be a contiguous {dtype} tensor of at least {n} entries on cuda:{dev}")
 
 
-def _launch(fn, dev: int, stream, *args):
-    """fn(*args, stream) with the tensors' device current, on `stream` or the device's current one."""
+# The calls' arguments, the stream last, as ``dspark_packed_call`` takes them: one foreign argument instead of 16 to 20.
+_PAGE_SLOTS, _NORM_ROPE, _ATTEND, _SAMPLE = (0, struct.Struct("@16q")), (1, struct.Struct("@13qd6q")), (2, struct.Struct("@10qd8q")), \
+    (3, struct.Struct("@15q"))
+
+
+def _launch(call, dev: int, stream, *args):
+    """The call with the tensors' device current, on `stream` or the device's current one."""
     import torch
     c = torch._C
-    s = stream.cuda_stream if stream is not None else c._cuda_getCurrentRawStream(dev)
-    cur = c._cuda_getDevice()
-    if cur == dev:
-        rc = fn(*args, s)
+    words = call[1].pack(*args, stream.cuda_stream if stream is not None else c._cuda_getCurrentRawStream(dev))
+    if c._cuda_getDevice() == dev:
+        rc = get_lib().dspark_packed_call(call[0], words)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, s)
+            rc = get_lib().dspark_packed_call(call[0], words)
     if rc != DSPARK_OK:
         _check(rc)
 
@@ -354,7 +364,7 @@ def page_slots(cache: PagedKvCache, ctx_len, n_new, n_pages, free_pages, free_co
     kv_len = new(B) if kv_len is None else kv_len
     slots = new(max_tokens, torch.int64) if slots is None else slots
     positions = new(max_tokens) if positions is None else positions
-    _launch(get_lib().dspark_page_slots, dev, stream,
+    _launch(_PAGE_SLOTS, dev, stream,
             cache.ref, _vec(ctx_len, "ctx_len", i32, B, dev), _vec(n_new, "n_new", i32, B, dev), B,
             _vec(n_pages, "n_pages", i32, B, dev), _vec(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
             _vec(free_count, "free_count", i32, 1, dev), max_tokens, _vec(n_pages_out, "n_pages_out", i32, B, dev),
@@ -397,10 +407,10 @@ def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: 
         q_out = _empty((T, nH, hd), cache.dtype, cache.device, stream)
     elif q_out.dtype is not cache.dtype or q_out.shape != q_shape or not q_out.is_contiguous() or q_out.get_device() != dev:
         _refuse("q_out must be a contiguous [T, heads, head_dim] tensor in the cache's dtype")
-    _launch(get_lib().dspark_norm_rope_paged, dev, stream,
-            cache.ref, layer, _dtype_code(dt), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, nH,
-            _vec(q_norm, "q_norm", dt, hd, dev) if q_norm is not None else None,
-            _vec(k_norm, "k_norm", dt, hd, dev) if k_norm is not None else None,
+    _launch(_NORM_ROPE, dev, stream,
+            cache.ref, layer, _dtype_code(dt), q.data_ptr(), qs, k.data_ptr(), ks, _addr(v), vs, nH,
+            _vec(q_norm, "q_norm", dt, hd, dev) if q_norm is not None else 0,
+            _vec(k_norm, "k_norm", dt, hd, dev) if k_norm is not None else 0,
             _vec(inv_freq, "inv_freq", torch.float64, hd // 2, dev), eps, 1 if v_norm else 0,
             _vec(positions, "positions", torch.int32, T, dev), _vec(slots, "slots", torch.int64, T, dev), T,
             q_out.data_ptr())
@@ -446,10 +456,10 @@ def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: in
         _refuse("lse must be a contiguous float32 tensor [T, heads]")
     if ws is None:
         ws = attend_paged_workspace(cache, T, nH, B, stream)
-    _launch(get_lib().dspark_attend_paged, dev, stream,
+    _launch(_ATTEND, dev, stream,
             cache.ref, layer, q.data_ptr(), qs, nH, _vec(cu_new, "cu_new", torch.int32, B + 1, dev),
             _vec(kv_len, "kv_len", torch.int32, B, dev), B, T, max_new, scale, 1 if causal else 0, window, out.data_ptr(),
-            os_, _ptr(lse), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
+            os_, _addr(lse), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
     return out
 
 
@@ -472,13 +482,13 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
         tokens = _empty(R, torch.int32, logits.device, stream)
     if ws is None:
         ws = sample_workspace(R, V, logits.device, stream)
-    _launch(get_lib().dspark_sample, dev, stream,
+    _launch(_SAMPLE, dev, stream,
             logits.data_ptr(), _dtype_code(logits.dtype), logits.stride(0), R, V, _vec(u, "u", f32, R, dev),
-            None if temperature is None else _vec(temperature, "temperature", f32, R, dev),
-            None if top_k is None else _vec(top_k, "top_k", torch.int32, R, dev),
-            None if top_p is None else _vec(top_p, "top_p", f32, R, dev),
-            None if min_p is None else _vec(min_p, "min_p", f32, R, dev), _vec(tokens, "tokens", torch.int32, R, dev),
-            None if probs is None else _vec(probs, "probs", f32, R, dev), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
+            0 if temperature is None else _vec(temperature, "temperature", f32, R, dev),
+            0 if top_k is None else _vec(top_k, "top_k", torch.int32, R, dev),
+            0 if top_p is None else _vec(top_p, "top_p", f32, R, dev),
+            0 if min_p is None else _vec(min_p, "min_p", f32, R, dev), _vec(tokens, "tokens", torch.int32, R, dev),
+            0 if probs is None else _vec(probs, "probs", f32, R, dev), _vec(ws, "ws", torch.uint8, 0, dev), ws.numel())
     return tokens
 
 

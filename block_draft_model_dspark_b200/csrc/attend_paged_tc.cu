@@ -4,13 +4,19 @@
 // A unit is up to NQ query tiles of one (request, kv head): the grp query heads
 // that share the kv head times tpt = 128 / grp tokens fill the 128 rows of a tile
 // (row r = token r / grp, head r % grp), so K and V are read once for all of them. Its
-// key tiles of KT rows are gathered from the pages by TMA, one request per page
-// and 64 dimensions, into the swizzled layout the MMAs read.
+// key tiles of KT rows are gathered from the pages by TMA, a copy per page
+// and 64 dimensions (one per page of 16 rows), into the swizzled layout the MMAs read.
 //   S = Q K^T -> TMEM (two buffers); P = exp2(scale log2(e) (S - m)) -> TMEM over
 //   its S buffer, in the cache's type (both operands of an MMA have one type;
 //   the sums take the unrounded P); O += P V -> TMEM.
 // The running maximum m is raised only when a tile's exceeds it by 8 (log2), so O
 // is rarely rescaled; P stays below 256.
+//
+// Bound by the K and V bytes for few new tokens (64 requests of 8K to 32K keys, one token each: 852 us, 6.05 TB/s; 6.6
+// with pages of 64), by the chain S -> softmax -> PV for prompt chunks (4 x 2048 tokens over up to 8K keys, head_dim 128:
+// 450 us, 1000 TFLOP/s, tensor pipe 53% active), by the loads for head_dim 256, whose tiles serve 128 rows only
+// (8191 tokens in a window of 1024: 182 us, 750 TFLOP/s; without the window 990). One request's 17 tokens over 4096
+// keys take 22 us: two launches, and a few microseconds each for finding the share, the first tile and the pieces' join.
 //
 // Steps: with NQ = 2 (prompt chunks, head_dim <= 128, KT = 128) step s is tile s / 2 of
 // query tile s % 2, with NQ = 1 it is tile s; step s uses S buffer s % 2. The
@@ -45,7 +51,7 @@ namespace tc {
 namespace {
 
 constexpr int kGrid = 148;           // shares: one CTA per SM of a B200
-constexpr int kUnitCost = 2;         // a unit's fixed work (query tile, first load, epilogue) in tiles
+constexpr int kUnitCost = 4;         // a unit's fixed work (query tile, first load, epilogue) in tiles (2 to 4 measure alike, 1 and 6 worse)
 constexpr int kRows = 128;           // rows of a query tile: the MMAs' M
 constexpr int kMaxBatch = 4096;
 constexpr float kRescale = 8.0f;     // log2 headroom before the running maximum is raised

@@ -10,7 +10,8 @@
 // of one cluster, each CTA scanning all requests (they sit in L2) into its own
 // shared memory, then a share of the fill per CTA. The cluster barrier between
 // the last read of a request's numbers and the first write lets the outputs
-// be the inputs' own arrays (lengths and page counts advanced in place).
+// be the inputs' own arrays (lengths and page counts advanced in place). One request takes
+// 6 us in a graph, 512 requests with 65,000 tokens 11.7 us.
 #include "paged.h"
 
 namespace dspark {
@@ -211,9 +212,10 @@ extern "C" int dspark_page_slots(const dspark_paged_cache* c, const int32_t* ctx
     P.cluster = 1;
     while (P.cluster < kMaxCluster && (int64_t)P.cluster * 2 * kThreads * kTok < max_tokens) P.cluster *= 2;
     const size_t smem = (4 * (size_t)B + 2) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((4 * kMaxBatch + 2) * sizeof(int32_t)));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaSuccess;                      // (the attributes cost host time: only where the launch needs them)
+    if (smem > 48 * 1024)
+        e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((4 * kMaxBatch + 2) * sizeof(int32_t)));
+    if (e == cudaSuccess && P.cluster > 8) e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
         e = launch_pdl_cluster(page_slots_kernel, dim3(P.cluster), dim3(kThreads), P.cluster, smem, static_cast<cudaStream_t>(stream), P);
     if (e != cudaSuccess) DSPARK_FAIL(DSPARK_ERR_CUDA, std::string("page slots launch: ") + cudaGetErrorString(e));

@@ -519,6 +519,16 @@ int dspark_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t
                   int32_t* tokens, float* probs, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * One of the four calls above with its arguments, in order, as 64-bit words: pointers and integers as they are,
+ * float arguments as the bits of a double. The same checks, result and errors.
+ */
+#define DSPARK_CALL_PAGE_SLOTS      0
+#define DSPARK_CALL_NORM_ROPE_PAGED 1
+#define DSPARK_CALL_ATTEND_PAGED    2
+#define DSPARK_CALL_SAMPLE          3
+int dspark_packed_call(int32_t call, const int64_t* words);
+
+/*
  * Test-facing dump of every layer's attention output (the parity check of the
  * DeepspecContextAttention.attend seam inside a round, page 75). While `dst`
  * is non-NULL, every later dspark_draft_rows call on `model` also copies each

@@ -125,3 +125,29 @@ def test_sample_refusals(dsp):
     assert need > 0 and lib.dspark_sample_workspace_bytes(-1, 100) == 0 and lib.dspark_sample_workspace_bytes(1, 0) == 0
     refused(dsp, lib.dspark_sample(*sample_args(ws_bytes=need - 1)), -4)
     assert lib.dspark_sample(*sample_args(rows=0, logits=None)) == 0
+
+
+def test_packed_calls_refuse_alike(dsp):
+    """The same call as a block of 64-bit words: the same result and message, argument by argument."""
+    import struct
+    lib, c = dsp.get_lib(), cache(dsp)
+
+    def both(call, plain, args):
+        words = struct.pack("@" + "".join("d" if isinstance(a, float) else "q" for a in args), *[0 if a is None else a for a in args])
+        want, msg = plain(*args), dsp.get_lib().dspark_last_error()
+        assert lib.dspark_packed_call(call, words) == want and dsp.get_lib().dspark_last_error() == msg
+        return want
+
+    for kw in (dict(B=9), dict(free_pages=None), dict(max_tokens=-1), dict(positions=None)):
+        assert both(0, lib.dspark_page_slots, slots_args(c, **kw)) == -1
+    for kw in (dict(layer=2), dict(x_dtype=7), dict(eps=-1.0), dict(k_stride=4), dict(q_out=None), dict(T=-1)):
+        assert both(1, lib.dspark_norm_rope_paged, norm_args(c, **kw)) == -1
+    assert both(1, lib.dspark_norm_rope_paged, norm_args(c, T=0)) == 0
+    for kw in (dict(scale=0.0), dict(window=-1), dict(B=9), dict(out_stride=100), dict(ws=None)):
+        assert both(2, lib.dspark_attend_paged, attend_args(c, **kw)) == -1
+    assert both(2, lib.dspark_attend_paged, attend_args(c, ws_bytes=8)) == -4
+    for kw in (dict(dtype=5), dict(row_stride=99), dict(tokens=None), dict(ws=P + 16)):
+        assert both(3, lib.dspark_sample, sample_args(**kw)) == -1
+    assert both(3, lib.dspark_sample, sample_args(rows=0)) == 0
+    refused(dsp, lib.dspark_packed_call(4, b"\0" * 160), -1)
+    refused(dsp, lib.dspark_packed_call(0, None), -1)
