@@ -158,3 +158,64 @@ def test_no_tokens_or_requests():
     dsp.attend_paged(torch.zeros_like(out), cache, 0, z[:1], z[:0], 0, 1.0, out=out)
     dsp.attend_paged(torch.zeros_like(out), cache, 0, z, z[:2], 5, 1.0, out=out)
     assert bool((out == 2.0).all()) and cache.read_status() == 0
+
+
+def test_lengths_that_cannot_be_are_reported():
+    """Negative lengths count as 0, offsets past the tokens as their end; rows that belong to nobody stay."""
+    import block_draft_model_dspark_b200 as dsp
+    rng = np.random.default_rng(30)
+    for hd, dt in ((128, torch.bfloat16), (256, torch.float16), (64, torch.float32)):
+        cache = make_paged(rng, [40, 50], 16, 2, hd, dt)
+        q = torch.from_numpy(rng.standard_normal((6, 4, hd)).astype(np.float32)).to(dt).cuda()
+        good = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+        for cu, kv in (([0, 2, 4], [-5, 50]), ([0, 2, 9], [40, 50])):
+            out = torch.full((6, 4, hd), 2.0, dtype=dt, device="cuda")
+            dsp.attend_paged(q, cache, 0, torch.tensor(cu, dtype=torch.int32, device="cuda"), torch.tensor(kv, dtype=torch.int32, device="cuda"), 5, 0.1, out=out)
+            status = cache.read_status()
+            if kv[0] < 0:
+                assert status == dsp.DSPARK_DEV_BAD_LENGTH and bool((out[:2] == 0).all()) and bool((out[4:] == 2.0).all())
+                ref = ref_attend(q[2:4], make_view(cache, 1), 0, [2], [50], 0.1, True, 0)
+                check_attend(out[2:4], None, ref, dt, 50, "the other request")
+            elif dt is not torch.float32:
+                assert status == dsp.DSPARK_DEV_BAD_LENGTH
+        out = torch.full((6, 4, hd), 2.0, dtype=dt, device="cuda")
+        dsp.attend_paged(q, cache, 0, good, torch.tensor([40, 50], dtype=torch.int32, device="cuda"), 2, 0.1, out=out)
+        assert cache.read_status() == 0 and bool((out[4:] == 2.0).all())
+
+
+def make_view(cache, b):
+    """The cache as request b sees it."""
+    import block_draft_model_dspark_b200 as dsp
+    return dsp.PagedKvCache(cache.num_pages, cache.page_size, cache.n_kv, cache.head_dim, block_table=cache.block_table[b:b + 1].contiguous(), k=cache.k, v=cache.v)
+
+
+@pytest.mark.parametrize("hd,page", [(64, 16), (128, 32)])
+def test_as_many_requests_as_a_call_takes(hd, page):
+    new = [(i * 7) % 3 for i in range(4096)]
+    run(31, new, [n + (i * 13) % 40 for i, n in enumerate(new)], 2, 1, hd, page, "bf16")
+
+
+def test_a_window_wider_than_the_request_is_none():
+    import block_draft_model_dspark_b200 as dsp
+    rng = np.random.default_rng(32)
+    cache = make_paged(rng, [300, 90], 16, 2, 128, torch.bfloat16)
+    q = torch.from_numpy(rng.standard_normal((40, 4, 128)).astype(np.float32)).bfloat16().cuda()
+    cu, kv = torch.tensor([0, 33, 40], dtype=torch.int32, device="cuda"), torch.tensor([300, 90], dtype=torch.int32, device="cuda")
+    for causal in (True, False):
+        want = dsp.attend_paged(q, cache, 0, cu, kv, 33, 0.1, causal=causal)
+        for window in (320, 1 << 20, 2 ** 31 - 1):
+            assert torch.equal(dsp.attend_paged(q, cache, 0, cu, kv, 33, 0.1, causal=causal, window=window), want)
+
+
+def test_max_new_only_chooses_tiles():
+    """The bound on a request's new tokens may be loose: results stay within their roundings."""
+    for max_new in (1, 500):
+        import block_draft_model_dspark_b200 as dsp
+        rng = np.random.default_rng(33)
+        new, kv_len = [70, 1, 16], [200, 90, 16]
+        cache = make_paged(rng, kv_len, 16, 2, 128, torch.bfloat16)
+        q = torch.from_numpy(rng.standard_normal((87, 8, 128)).astype(np.float32)).bfloat16().cuda()
+        cu, kv = torch.tensor([0, 70, 71, 87], dtype=torch.int32, device="cuda"), torch.tensor(kv_len, dtype=torch.int32, device="cuda")
+        lse = torch.zeros(87, 8, device="cuda")
+        out = dsp.attend_paged(q, cache, 0, cu, kv, max_new, 0.09, lse=lse)
+        check_attend(out, lse, ref_attend(q, cache, 0, new, kv_len, 0.09, True, 0), torch.bfloat16, 200, max_new)

@@ -118,3 +118,19 @@ def test_page_slots_bad_page_gives_no_slot():
     cu, kv, slots, pos, _, _ = dsp.page_slots(cache, dev([10]), dev([16]), dev([2]), dev([4]), dev([1]), 16)
     assert slots.tolist() == [3 * 16 + 10 + i for i in range(6)] + [-1] * 10
     assert cache.read_status() == dsp.DSPARK_DEV_BAD_PAGE
+
+
+def test_many_tokens_over_a_cluster():
+    """Sizes at which one, several and sixteen CTAs share the fill, in place."""
+    import block_draft_model_dspark_b200 as dsp
+    for seed, B, new_hi, pad in ((40, 3, 1000, 0), (41, 700, 40, 7), (42, 4096, 30, 1), (43, 2, 60000, 13)):
+        ctx, new, held, free, table, pages = case(seed, B, 16, 300, new_hi)
+        total = sum(new) + pad
+        cache = cache_of(table, pages, 16)
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        c, n, h, cnt = i32(ctx), i32(new), i32(held), i32([len(free)])
+        cu, kv, slots, pos, _, _ = dsp.page_slots(cache, c, n, h, torch.from_numpy(free).cuda(), cnt, total, n_pages_out=h, free_count_out=cnt, kv_len=c)
+        want = ref_page_slots(ctx, new, held, free, len(free), table, 16, total)
+        assert h.tolist() == want[0] and int(cnt) == want[1] and cu.tolist() == want[2] and c.tolist() == want[3]
+        assert slots.tolist() == want[4] and pos.tolist() == want[5] and np.array_equal(cache.block_table.cpu().numpy(), want[6])
+        assert cache.read_status() == 0
