@@ -10,7 +10,7 @@
 // rotation needs no exchange and its eight cosines and sines stay in registers from head to head; the sum of squares is
 // a shuffle over the head's lanes. The angles: the turn count is reduced in 64 bits (at position 10^6 a 32-bit angle
 // is off by 0.03 rad), sine and cosine are taken of the fraction in 32 bits, each once a warp.
-// 16384 tokens of 48 bf16 heads of 128: 90 us, 4.5 TB/s (of 6.55 measured for a copy); the instructions and the
+// 16384 tokens of 48 bf16 heads of 128: 85 us, 4.7 TB/s (of 6.55 measured for a copy); the instructions and the
 // registers for loads in flight share what is left.
 #include "paged.h"
 
@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Heads of a thread whose loads are in flight together, and the blocks an SM has registers for. Measured: 16384 tokens of 48
-// bf16 heads of 128 take 90 us so, 97 to 147 us with three or four heads, or the next round's loads ahead (registers);
+// bf16 heads of 128 take 85 us so, 7 to 57 us more with three or four heads, or the next round's loads ahead (registers);
 // fp32 rows (twice the bytes a load) gain from two heads what a third block gives.
 constexpr int kItems = 2;
 template <typename X> constexpr int kBlocksOf = sizeof(X) == 4 ? 2 : 3;
@@ -31,8 +31,8 @@ struct NormRopeParams {
     void* q_out; void* kc; void* vc;
     int32_t* status;
     int64_t num_slots;
-    int T, nH, nKv, hd, lanes, v_norm, split;   // lanes: threads per head (a power of two, at most 16); split: warps per token
-    float eps;
+    int T, nH, nKv, hd, lanes, log_lanes, v_norm, split, log_split;   // lanes: threads per head (a power of two, at most 16); split: warps per token
+    float eps, inv_hd;
 };
 
 template <typename T> struct Raw8;             // eight elements as loaded
@@ -79,13 +79,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
 
 template <typename X, typename O>
 __global__ void __launch_bounds__(kThreads, kBlocksOf<X>) norm_rope_kernel(NormRopeParams P) {
-    const int lane = threadIdx.x & 31, half = P.hd / 2, groups = 32 / P.lanes;
+    const int lane = threadIdx.x & 31, half = P.hd / 2, groups = 32 >> P.log_lanes;
     const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
-    const int t = (int)(w / P.split), part = (int)(w - (int64_t)t * P.split);
+    const int t = (int)(w >> P.log_split), part = (int)w & (P.split - 1);
     if (t >= P.T) return;
-    const int grp = lane / P.lanes, l = lane % P.lanes, e = l * 8;
+    const int grp = lane >> P.log_lanes, l = lane & (P.lanes - 1), e = l * 8;
     const bool mine = e < half;                 // hd = 192 and the like leave lanes idle
     const int heads = P.nH + 2 * P.nKv;
     int64_t slot = P.slots[t];
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksOf<X>) norm_rope_kernel(NormR
             }
             if (slot < 0) return;               // a padding row
             // a lane's eight pairs: its group finds 8 / groups of them, the groups tell each other
-            const int each = groups >= 8 ? 1 : 8 / groups;    // 1, 2 or 4
+            const int shift = groups >= 8 ? 0 : groups == 4 ? 1 : 2, each = 1 << shift;
             float c[4], s[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksOf<X>) norm_rope_kernel(NormR
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int from = i / each * P.lanes + l;
+                const int from = (i >> shift) * P.lanes + l;
                 const float ci = each == 4 ? c[i & 3] : each == 2 ? c[i & 1] : c[0], si = each == 4 ? s[i & 3] : each == 2 ? s[i & 1] : s[0];
                 cs[i] = __shfl_sync(0xffffffffu, ci, from);
                 sn[i] = __shfl_sync(0xffffffffu, si, from);
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksOf<X>) norm_rope_kernel(NormR
             }
             for (int o = P.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             if (!on) continue;                  // lanes of a head agree except idle ones; the shuffle is behind
-            const float r = kind == 2 && !P.v_norm ? 1.f : 1.f / sqrtf(ss / (float)P.hd + P.eps);
+            // (rsqrtf is within 2^-22: far inside the one rounding to 16 bits, and 4 of the squares' roundings in fp32)
+            const float r = kind == 2 && !P.v_norm ? 1.f : rsqrtf(ss * P.inv_hd + P.eps);
             if (kind == 2) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) { x1[j] *= r; x2[j] *= r; }
@@ -227,11 +228,12 @@ extern "C" int dspark_norm_rope_paged(const dspark_paged_cache* c, int32_t layer
     P.vc = static_cast<char*>(c->v) + layer_bytes;
     P.status = c->status; P.num_slots = (int64_t)c->num_pages * c->page_size;
     P.T = T; P.nH = n_heads; P.nKv = c->n_kv; P.hd = c->head_dim; P.v_norm = v_norm != 0; P.eps = eps;
+    P.inv_hd = 1.f / (float)c->head_dim;
     P.lanes = 1;
-    while (P.lanes * 16 < P.hd) P.lanes *= 2;
+    while (P.lanes * 16 < P.hd) { P.lanes *= 2; ++P.log_lanes; }
     // few tokens: a token's heads over several warps, until the SMs have a block each or a warp has one round
     P.split = 1;
-    while ((int64_t)T * P.split < 148 * 8 && P.split * (32 / P.lanes) < n_heads + 2 * c->n_kv) P.split *= 2;
+    while ((int64_t)T * P.split < 148 * 8 && P.split * (32 / P.lanes) < n_heads + 2 * c->n_kv) { P.split *= 2; ++P.log_split; }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = x_dtype == DSPARK_DTYPE_F32 ? launch_x<float>(P, c->dtype, s)
                   : x_dtype == DSPARK_DTYPE_F16 ? launch_x<__half>(P, c->dtype, s)
