@@ -30,9 +30,9 @@
 // of them share a bank) times the Taylor polynomial of degree 6 on |r| <= 1/32 octave, within
 // 2^-46: 12 64-bit operations an element.
 //
-// 512 rows of 262144 fp32 logits: greedy 137 us (3.9 TB/s), top-k 210 us (two passes over the row), unfiltered 285 us
-// (the 64-bit operations), top-p 480 to 800 us (a third and a fourth pass, or a fifth far down the tail). One such row:
-// 9 to 45 us, the exchanges of its 16 CTAs.
+// 512 rows of 262144 fp32 logits: greedy 135 us (4.0 TB/s), top-k 228 us (two passes over the row), unfiltered 288 us
+// (the 64-bit operations), top-p 480 to 790 us (a third and a fourth pass, or a fifth far down the tail). One such row:
+// 8 to 42 us, the exchanges of its 16 CTAs.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -191,9 +191,11 @@ __device__ __forceinline__ double block_scan(double v, double* buf, double* tota
     *total = all;
     return base + before;
 }
-// Falling bitonic sort of n (a power of two, 64 .. kList) entries. Pairs at most 32 apart
+// Falling bitonic sort of n (a power of two, 64 .. kList) entries; a constant, so that the loops unroll, and a call,
+// so that they do not crowd the passes' registers. Pairs at most 32 apart
 // stay within one warp's 64 entries.
-__device__ void sort_falling(uint64_t* a, int n) {
+template <int n>
+__device__ __noinline__ void sort_falling(uint64_t* a) {
     const int tid = threadIdx.x;
     __syncthreads();
     for (int k = 2; k <= n; k <<= 1) {
@@ -358,13 +360,13 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         for (int i = tid; i < parts * NT; i += NT) list[i] = (uint64_t)order_key(parts == 1 ? best : -INFINITY) << 32;
         if (parts > 1) {
             int part = 0;
-            scan(Light{}, v0 + lane, v1, 32, !P.resident, [&](const float (&)[VEC], int, float hi) {
+            scan(std::integral_constant<int, 1>{}, v0 + lane, v1, 32, !P.resident, [&](const float (&)[VEC], int, float hi) {
                 uint64_t& most = list[part * NT + tid];
                 most = max(most, (uint64_t)order_key(hi) << 32);
                 part = part + 1 == parts ? 0 : part + 1;
             });
         }
-        sort_falling(list, parts * NT);
+        if (parts == 1) sort_falling<NT>(list); else sort_falling<kList>(list);
         bound = key_value((uint32_t)(list[k - 1] >> 32));
         share = key_value((uint32_t)(list[(k - 1) / C] >> 32));
         tell(S.x.share, (double)share);
@@ -461,11 +463,18 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
         meet();
         return sum_of(S.x.listed);
     };
+    auto resort = [&](int m) {
+        if (m == 256) sort_falling<256>(list);
+        else if (m == 512) sort_falling<512>(list);
+        else if (m == 1024) sort_falling<1024>(list);
+        else if (m == 2048) sort_falling<2048>(list);
+        else sort_falling<kList>(list);
+    };
     auto sort_list = [&](int n) {
-        int m = 64;
+        int m = 256;
         while (m < n) m *= 2;
         for (int i = n + tid; i < m; i += NT) list[i] = 0;
-        sort_falling(list, m);
+        resort(m);
         return m;
     };
     // CTA 0 finishes the row from its list of n entries, the only ones that can stay; total: top-p's whole (without top-k).
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
             // next by rising index: complements fall
             list[q] = keep ? ~(((uint64_t)(0xffffffffu - (uint32_t)e) << 32) | (uint32_t)(e >> 32)) : 0;
         }
-        sort_falling(list, m);
+        resort(m);
         mine = 0.0;
         int last = -1;
         for (int i = 0, q = tid * per; i < per && q < m; ++i, ++q) {
