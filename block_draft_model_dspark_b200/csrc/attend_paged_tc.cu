@@ -6,7 +6,7 @@
 // (row r = token r / grp, head r % grp), so K and V are read once for all of them. Its
 // key tiles of KT rows are gathered from the pages by TMA, a copy per page
 // and 64 dimensions (one per page of 16 rows), into the swizzled layout the MMAs read.
-//   S = Q K^T -> TMEM (two buffers); P = exp2(scale log2(e) (S - m)) -> TMEM over
+//   S = Q K^T -> TMEM; P = exp2(scale log2(e) (S - m)) -> TMEM over
 //   its S buffer, in the cache's type (both operands of an MMA have one type;
 //   the sums take the unrounded P); O += P V -> TMEM.
 // The running maximum m is raised only when a tile's exceeds it by 8 (log2), so O

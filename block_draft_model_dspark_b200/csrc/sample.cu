@@ -33,7 +33,6 @@
 // 512 rows of 262144 fp32 logits: greedy 135 us (4.0 TB/s), top-k 228 us (two passes over the row), unfiltered 288 us
 // (the 64-bit operations), top-p 480 to 790 us (a third and a fourth pass, or a fifth far down the tail). One such row:
 // 8 to 42 us, the exchanges of its 16 CTAs.
-#include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
