@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     if (tid < 16) S.tab[tid] = exp2((double)tid * 0.0625);
     pdl_trigger();
     pdl_wait();
+    __syncthreads();                                          // the table: the first pass over a streamed row sums weights already
     const float T = P.temperature ? P.temperature[r] : 1.f, p = P.top_p ? P.top_p[r] : 1.f, mp = P.min_p ? P.min_p[r] : 0.f, u = P.u[r];
     const int k = P.top_k ? P.top_k[r] : 0;
     const bool alone = !(T > 0.f) || p <= 0.f || mp > 1.f || k == 1;                    // greedy, or a filter that leaves one

@@ -164,3 +164,29 @@ def test_top_k_of_every_size(R):
     for k in (1, 2, 511, 512, 513, 1500, 2047, 2048, 2049, 30010):
         check(x, u, top_k=np.full(R, k, np.int32))
     check(x, u, top_k=rng.integers(400, 2300, R).astype(np.int32), top_p=np.full(R, 0.95, np.float32), min_p=np.full(R, 0.001, np.float32))
+
+
+def test_streamed_rows_on_dirty_shared_memory():
+    """Rows that one CTA streams sum weights in their first pass already: the table of powers they read is complete by then,
+    whatever the kernel before left in shared memory."""
+    import block_draft_model_dspark_b200 as dsp
+    R, V = 300, 20011                                             # more rows than places, 80 KB a row: none is kept
+    x, rng = logits(10, R, V, "fp32")
+    u = rng.random(R, dtype=np.float32)
+    table = torch.zeros(R, 1, dtype=torch.int32, device="cuda")
+    cache = dsp.PagedKvCache(1, 16, 1, 128, block_table=table, dtype=torch.float16)
+    q = torch.full((R * 130, 1, 128), 6e4, dtype=torch.float16, device="cuda")        # as the powers of the table: 1e286
+    cu = torch.arange(R + 1, dtype=torch.int32, device="cuda") * 130
+    kv = torch.full((R,), 16, dtype=torch.int32, device="cuda")
+    xd, ud = x.cuda(), torch.from_numpy(u).cuda()
+    for kw in (dict(temperature=np.full(R, 0.9, np.float32)), dict(top_p=np.full(R, 0.9, np.float32))):
+        check(x, u, **kw)
+        dev = {k: torch.from_numpy(v).cuda() for k, v in kw.items()}
+        want, share = dsp.sample(xd, ud, **dev), torch.zeros(R, device="cuda")
+        for _ in range(20):
+            dsp.attend_paged(q, cache, 0, cu, kv, 130, 1.0)       # fills every SM's shared memory with its queries
+            probs = torch.zeros(R, device="cuda")
+            got = dsp.sample(xd, ud, probs=probs, **dev)
+            assert torch.equal(got, want)
+            share = probs if not share.any() else share
+            assert torch.equal(probs, share)
