@@ -1,4 +1,6 @@
 """sample against float64: tokens equal, shares within the roundings of one division and one fp32 result."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -190,3 +192,43 @@ def test_streamed_rows_on_dirty_shared_memory():
             assert torch.equal(got, want)
             share = probs if not share.any() else share
             assert torch.equal(probs, share)
+
+
+@pytest.mark.parametrize("dt,V,near,below", [("fp32", 5_100_001, 4_330_000, 0.98 / 64), ("fp16", (1 << 24) - 1, 15_500_000, 9 * 2.0 ** -11)])
+def test_millions_of_logits_in_one_bin(dt, V, near, below):
+    """One CTA's share of top-p's histogram with millions of entries in the maximum's bin, `below` the maximum, where
+    their places (in 1 / 1024 of a bin) add up to more than 2^32, and a thin tail in which the prefix ends."""
+    import block_draft_model_dspark_b200 as dsp
+    R = 150                                                       # more than half the places: a CTA per row
+    rng = np.random.default_rng(V)
+    x = torch.empty(V)
+    x[:near] = 1.0 - below
+    x[77] = 1.0
+    x[near:] = torch.from_numpy(0.9 - rng.random(V - near) * (V - near) / (64 * 1500)).float()      # 1500 a bin
+    x = x.to(DT[dt]).cuda()
+    share = float(torch.exp(x[near:].double() - 1).sum() / torch.exp(x.double() - 1).sum())        # the tail's
+    p = (1 - share * rng.uniform(0.03, 0.15, R)).astype(np.float32)
+    u = rng.uniform(1 - 2 * share, 1.0, R).astype(np.float32)
+    probs = torch.zeros(R, device="cuda")
+    tok = dsp.sample(x.expand(R, V).contiguous(), torch.from_numpy(u).cuda(), top_p=torch.from_numpy(p).cuda(), probs=probs).cpu()
+    order = torch.argsort(x, descending=True, stable=True)
+    rank = torch.empty_like(order)
+    rank[order] = torch.arange(V, device="cuda")
+    # exact sums here: whole numbers of 2^-38 (V of them stay below 2^63). They are off by V 2^-39 at most, the kernel's by its
+    # weights (2^-45, twice where a maximum changes) and the additions of a thread's chain, V / 1024 of them, and of the join
+    w = torch.round(torch.exp(x.double() - 1) * 2.0 ** 38).long()
+    before = (torch.cumsum(w[order], 0) - w[order]).double() * 2.0 ** -38
+    total, told = float(w.sum()) * 2.0 ** -38, 0
+    off = V * 2.0 ** -38 + 2 * total * ((V / 1024 + 64) * 2.0 ** -53 + 2.0 ** -44)
+    for r in range(R):
+        n = int((before < float(p[r]) * total).sum())
+        c = torch.cumsum(torch.where(rank < n, w, torch.zeros_like(w)), 0).double() * 2.0 ** -38
+        want = float(u[r]) * float(c[-1])
+        if min(float((before - float(p[r]) * total).abs().min()), float((c - want).abs().min())) < off:
+            continue
+        told += 1
+        at = int((c <= want).sum())
+        assert int(tok[r]) == at, (r, int(tok[r]), at)
+        prob = math.exp(float(x[at]) - 1) / float(c[-1])
+        assert abs(float(probs[r]) - prob) <= 2.0 ** -23 * prob
+    assert told > R // 2
