@@ -22,6 +22,7 @@ constexpr int kThreads = 512;
 constexpr int kPer = kMaxBatch / kThreads;   // requests per thread
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kScanBytes = 2 * kWarps * (int)sizeof(int64_t);
 constexpr int kTok = 4;                      // neighbouring tokens per thread
 
 struct SlotsParams {
@@ -69,7 +70,8 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(SlotsParams P) {
     int32_t* s_first = sm + P.B + 1;          // [B + 1] rank of the first page taken
     int32_t* s_ctx = s_first + P.B + 1;       // [B]
     int32_t* s_held = s_ctx + P.B;            // [B]
-    __shared__ int64_t buf[2][kWarps];
+    __shared__ int64_t buf[2][kWarps];        // kScanBytes
+    static_assert(sizeof(buf) == kScanBytes, "the kernel's static shared memory");
     const int tid = threadIdx.x, rank = P.cluster > 1 ? (int)blockIdx.x : 0;
     pdl_trigger();
     pdl_wait();
@@ -213,7 +215,7 @@ extern "C" int dspark_page_slots(const dspark_paged_cache* c, const int32_t* ctx
     while (P.cluster < kMaxCluster && (int64_t)P.cluster * 2 * kThreads * kTok < max_tokens) P.cluster *= 2;
     const size_t smem = (4 * (size_t)B + 2) * sizeof(int32_t);
     cudaError_t e = cudaSuccess;                      // (the attributes cost host time: only where the launch needs them)
-    if (smem > 48 * 1024)
+    if (smem > 48 * 1024 - kScanBytes)                // (48 KB without asking, the scans' buffers among them)
         e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((4 * kMaxBatch + 2) * sizeof(int32_t)));
     if (e == cudaSuccess && P.cluster > 8) e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)

@@ -1,5 +1,9 @@
 """page_slots against plain loops: exact, with ragged and empty requests, odd page sizes, in-place outputs,
 refusals that leave everything as it was, and pages outside the pool."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +12,7 @@ from paged_util import ceil_div, ref_page_slots
 from parity_util import ensure_built
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -134,3 +139,18 @@ def test_many_tokens_over_a_cluster():
         assert h.tolist() == want[0] and int(cnt) == want[1] and cu.tolist() == want[2] and c.tolist() == want[3]
         assert slots.tolist() == want[4] and pos.tolist() == want[5] and np.array_equal(cache.block_table.cpu().numpy(), want[6])
         assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("B", [3055, 3056, 3071, 3072])
+def test_tables_around_the_default_shared_memory(B):
+    """The largest batches that fit it and the first that do not, each as the first call of a process (the opt-in to more
+    stays with the kernel once it is made)."""
+    code = ("import torch, block_draft_model_dspark_b200 as dsp\n"
+            f"B = {B}\n"
+            "i32 = dict(dtype=torch.int32, device='cuda')\n"
+            "cache = dsp.PagedKvCache(B, 16, 1, 16, batch=B, max_pages=1)\n"
+            "one, none = torch.ones(B, **i32), torch.zeros(B, **i32)\n"
+            "cu, kv, slots, pos, held, count = dsp.page_slots(cache, none, one, none, torch.arange(B, **i32), torch.tensor([B], **i32), B)\n"
+            "assert cu.tolist() == list(range(B + 1)) and slots.tolist() == [16 * (B - 1 - i) for i in range(B)] and int(count) == 0\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
