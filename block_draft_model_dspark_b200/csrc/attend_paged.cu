@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_paged_simt_kernel(PagedAtt
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float mn = fmaxf(m, mx);
-        if (mn == -INFINITY) continue;                 // scores of -infinity alone: nothing yet
-        const float f = __expf(m - mn), p = __expf(s - mn);
+        const float at = mn == -INFINITY ? 0.f : mn;   // (scores of -infinity alone so far: weights 0; a NaN: a sum that is none)
+        const float f = __expf(m - at), p = __expf(s - at);
         m = mn;
         l = l * f + warp_sum(p);
 #pragma unroll
@@ -88,12 +88,12 @@ __global__ void __launch_bounds__(kWarps * 32) attend_paged_simt_kernel(PagedAtt
                 if (lane + 32 * i < P.hd) acc[i] = fmaf(pj, to_f(vr[lane + 32 * i]), acc[i]);
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;         // a query that sees no key: zeros, lse -infinity
+    const float inv = l == 0.f ? 0.f : 1.f / l;        // a query that sees no key: zeros, lse -infinity
     T* o = static_cast<T*>(P.out) + t * P.out_stride + (int64_t)h * P.hd;
 #pragma unroll
     for (int i = 0; i < kMaxHd / 32; ++i)
         if (lane + 32 * i < P.hd) o[lane + 32 * i] = from_f<T>(acc[i] * inv);
-    if (P.lse && lane == 0) P.lse[(int64_t)t * P.nH + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    if (P.lse && lane == 0) P.lse[(int64_t)t * P.nH + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 }  // namespace

@@ -278,9 +278,15 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The largest; a NaN wins, so that a row's maximum tells of it (the polynomial below would hide one).
+__device__ __forceinline__ float max2(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 // Two fp32 lanes in one register pair: one instruction for both.
@@ -740,12 +746,12 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
                 }
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float top = max2(max2(mx[0], mx[1]), max2(mx[2], mx[3]));
                 if (SP == 2) mine[(t & 1) * 256] = top;       // two sets in turn: the other thread may still read the last
                 if (!agree(good)) { ok = false; break; }
-                if (SP == 2) top = fmaxf(top, other[(t & 1) * 256]);
+                if (SP == 2) top = max2(top, other[(t & 1) * 256]);
                 top *= c;
-                const bool need = m > -INFINITY && top > m + kRescale;
+                const bool need = m > -INFINITY && !(top <= m + kRescale);        // (a NaN becomes the maximum and stays it)
                 if (__any_sync(0xffffffffu, need && live)) {
                     // O holds the tiles before at the old maximum: their PV must have landed
                     good = wait(&B.odone[last_step & 1], (uint32_t)(last_step >> 1) & 1u);
@@ -823,7 +829,10 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 l += other[(now.nt & 1) * 256];
                 named_barrier_sync(1, 256);                   // both have read: the next piece may write
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            // l = 0: no key, or scores of -infinity alone (the polynomial's least value is 2^-126). A maximum that is NaN or
+            // +infinity (a query with a NaN, a score that overflowed) has no softmax: the row becomes NaN.
+            l = m == -INFINITY ? 0.f : m < INFINITY ? l : __int_as_float(0x7fffffff);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t tok = now.r.t0 + i;
             const int h = now.g * grp + head_r;
             if (now.whole) {
@@ -842,17 +851,17 @@ attend_paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                         tmem_ld_wait();
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = l > 0.f ? pack2<T>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv) : 0u;
+                    for (int j = 0; j < 16; ++j) w[j] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
                     transpose_blocks(w, lane);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (row_at[k] >= 0) *reinterpret_cast<uint4*>(out + row_at[k] + d) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                 }
-                if (valid && half == 0 && P.a.lse) P.a.lse[tok * P.a.nH + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                if (valid && half == 0 && P.a.lse) P.a.lse[tok * P.a.nH + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             } else {
                 // [slot][column / 4][row] float4: a warp's rows are neighbours
                 const int64_t part = (int64_t)now.slot * NQ + q;
-                if (valid && half == 0) P.part_ml[part * kRows + r] = make_float2(l > 0.f ? m : -INFINITY, l);
+                if (valid && half == 0) P.part_ml[part * kRows + r] = make_float2(l > 0.f ? m : l == 0.f ? -INFINITY : l, l);     // (no number: the whole row is none)
                 float4* po = P.part_o + (part * (HD / 4) + half * (OH / 4)) * kRows + r;
 #pragma unroll
                 for (int d = 0; d < OH; d += 32) {
@@ -922,10 +931,10 @@ __global__ void __launch_bounds__(32 * kMergeCols) attend_paged_merge_kernel(Par
             acc.x = fmaf(w, o[k].x, acc.x); acc.y = fmaf(w, o[k].y, acc.y); acc.z = fmaf(w, o[k].z, acc.z); acc.w = fmaf(w, o[k].w, acc.w);
         }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
     T* out = static_cast<T*>(P.a.out) + (int64_t)(req.t0 + i) * P.a.out_stride + (int64_t)h * HD + col * 4;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
-    if (P.a.lse && col == 0) P.a.lse[(int64_t)(req.t0 + i) * P.a.nH + h] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+    if (P.a.lse && col == 0) P.a.lse[(int64_t)(req.t0 + i) * P.a.nH + h] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host

@@ -470,8 +470,8 @@ int dspark_norm_rope_paged(const dspark_paged_cache* cache, int32_t layer, int32
  * j < kv_len[b], with causal j <= its own, with window > 0 also j > its own -
  * window. Query head h reads kv head h / (n_heads / n_kv):
  *   out[t,h] = sum_j softmax_j(scale q[t,h] . K[j,g]) V[j,g],  lse[t,h] = log sum_j exp(scale q . K[j])
- * A query that sees no key gets zeros and lse = -infinity; rows of no request
- * (at or past cu_new[B]) stay as they were.
+ * A query that sees no key, or whose scores are all -infinity, gets zeros and lse = -infinity; one with a
+ * NaN, or with a score of +infinity, gets NaN in both. Rows of no request (at or past cu_new[B]) stay as they were.
  *   q    device KV [T][n_heads][head_dim], q_stride elements between tokens
  *   cu_new  device int32 [B + 1], ascending, at most T; kv_len device int32 [B]
  *   max_new host: an upper bound of n over the requests (chooses the kernel's tiles)

@@ -219,3 +219,68 @@ def test_max_new_only_chooses_tiles():
         lse = torch.zeros(87, 8, device="cuda")
         out = dsp.attend_paged(q, cache, 0, cu, kv, max_new, 0.09, lse=lse)
         check_attend(out, lse, ref_attend(q, cache, 0, new, kv_len, 0.09, True, 0), torch.bfloat16, 200, max_new)
+
+
+@pytest.mark.parametrize("nH,nKv,hd,dt", [(4, 2, 128, "bf16"), (16, 2, 256, "fp16"), (4, 2, 64, "fp16"), (4, 2, 48, "bf16"), (2, 2, 64, "fp32")])
+@pytest.mark.parametrize("new,kv_len", [([3, 150, 2], [3, 400, 40]), ([1, 17], [1, 9000])])
+def test_queries_that_are_not_numbers(nH, nKv, hd, dt, new, kv_len):
+    """A NaN in a query makes its row NaN and its lse NaN, in one piece or joined from several, and no other row; without
+    a key to see, it stays zeros."""
+    import block_draft_model_dspark_b200 as dsp
+    rng = np.random.default_rng(40)
+    dtype, nan = DT[dt], float("nan")
+    cache = make_paged(rng, kv_len, 16, nKv, hd, dtype)
+    T = sum(new)
+    q = torch.from_numpy(rng.standard_normal((T, nH, hd)).astype(np.float32)).to(dtype)
+    bad = torch.from_numpy(rng.random((T, nH)) < 0.3)
+    bad[T - 1, 0], bad[0, 0] = True, True
+    q[bad, int(rng.integers(0, hd))] = nan
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    kv = torch.tensor(kv_len, dtype=torch.int32, device="cuda")
+    for causal, window in ((True, 0), (False, 0), (True, 33)):
+        lse = torch.zeros(T, nH, device="cuda")
+        out = dsp.attend_paged(q.cuda(), cache, 0, cu, kv, max(new), hd ** -0.5, causal=causal, window=window, lse=lse).cpu()
+        lse = lse.cpu()
+        assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+        clean = torch.where(bad[..., None], torch.zeros((), dtype=dtype), q)
+        ref = ref_attend(clean, cache, 0, new, kv_len, hd ** -0.5, causal, window)
+        zero = torch.where(bad[..., None], ref[0], out.double())
+        check_attend(zero, torch.where(bad, ref[2], lse.double()), ref, dtype, max(kv_len), "the other rows")
+        assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("nH,nKv,hd,dt", [(4, 2, 128, "bf16"), (16, 2, 256, "fp16"), (4, 2, 48, "bf16")])
+def test_not_a_number_without_a_key_is_zeros(nH, nKv, hd, dt):
+    import block_draft_model_dspark_b200 as dsp
+    cache = make_paged(np.random.default_rng(41), [2, 0], 16, nKv, hd, DT[dt])
+    q = torch.full((150 + 3, nH, hd), float("nan"), dtype=DT[dt], device="cuda")
+    lse = torch.zeros(153, nH, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = dsp.attend_paged(q, cache, 0, torch.tensor([0, 150, 153], **i32), torch.tensor([2, 0], **i32), 150, 1.0, lse=lse)
+    none = torch.ones(153, dtype=torch.bool)
+    none[148:150] = False                                         # the two that sit at keys
+    assert bool((out[none.cuda()] == 0).all()) and bool((lse[none.cuda()] == -float("inf")).all())
+    assert bool(out[148:150].isnan().all()) and bool(lse[148:150].isnan().all())
+
+
+@pytest.mark.parametrize("hd,dt", [(128, "bf16"), (256, "fp16"), (48, "fp16")])
+def test_one_infinite_score_is_not_a_number(hd, dt):
+    """q . K = +infinity for one key alone, whichever column of a tile it is: infinity less infinity. -infinity for all: zeros."""
+    import block_draft_model_dspark_b200 as dsp
+    i32 = dict(dtype=torch.int32, device="cuda")
+    L = 300
+    cache = dsp.PagedKvCache(L // 16 + 1, 16, 1, hd, block_table=torch.arange(L // 16 + 1, **i32)[None].contiguous(), dtype=DT[dt])
+    q = torch.ones(1, 1, hd, dtype=DT[dt], device="cuda")
+    q[:, 0, 3] = float("inf")
+    cache.k.view(-1, hd)[:, 3] = -1.0                             # the others: -infinity
+    cache.v.fill_(0.5)
+    cu, kv = torch.tensor([0, 1], **i32), torch.tensor([L], **i32)
+    lse = torch.zeros(1, 1, device="cuda")
+    out = dsp.attend_paged(q, cache, 0, cu, kv, 1, 0.1, lse=lse)
+    assert bool((out == 0).all()) and float(lse) == -float("inf")
+    for j in range(L):
+        cache.k.view(-1, hd)[j, 3] = 1.0
+        lse = torch.zeros(1, 1, device="cuda")
+        out = dsp.attend_paged(q, cache, 0, cu, kv, 1, 0.1, lse=lse)
+        assert bool(out.isnan().all()) and bool(lse.isnan().all()), j
+        cache.k.view(-1, hd)[j, 3] = -1.0
