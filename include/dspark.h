@@ -520,7 +520,8 @@ int dspark_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t
 
 /*
  * One of the four calls above with its arguments, in order, as 64-bit words: pointers and integers as they are,
- * float arguments as the bits of a double. The same checks, result and errors.
+ * float arguments as the bits of a double. The same checks, result and errors; a word that an int32_t argument
+ * does not hold is refused (DSPARK_ERR_INVALID_ARGUMENT).
  */
 #define DSPARK_CALL_PAGE_SLOTS      0
 #define DSPARK_CALL_NORM_ROPE_PAGED 1

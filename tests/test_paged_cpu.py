@@ -151,3 +151,19 @@ def test_packed_calls_refuse_alike(dsp):
     assert both(3, lib.dspark_sample, sample_args(rows=0)) == 0
     refused(dsp, lib.dspark_packed_call(4, b"\0" * 160), -1)
     refused(dsp, lib.dspark_packed_call(0, None), -1)
+
+
+def test_packed_integers_past_32_bits_are_refused(dsp):
+    """Not cut to their low half. Each call has another fault too (a NULL, a scale of 0), so that none could ever launch."""
+    import struct
+    lib, c = dsp.get_lib(), cache(dsp)
+    calls = [(0, slots_args(c, slots=None), (3, 6, 8)), (1, norm_args(c, q_out=None), (1, 2, 9, 14, 17)),
+             (2, attend_args(c, scale=0.0), (1, 4, 7, 8, 9, 11, 12)), (3, sample_args(tokens=None), (1, 3, 4))]
+    for call, args, where in calls:
+        for i in where:
+            for far in (1 << 32, -(1 << 32), 1 << 31, 1 << 62):
+                bad = [0 if a is None else a for a in args]
+                bad[i] += far
+                words = struct.pack("@" + "".join("d" if isinstance(a, float) else "q" for a in bad), *bad)
+                refused(dsp, lib.dspark_packed_call(call, words), -1)
+                assert b"32 bits" in lib.dspark_last_error(), (call, i, far, lib.dspark_last_error())
