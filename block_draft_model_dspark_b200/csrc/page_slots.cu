@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(SlotsParams P) {
     const int stride = kThreads * P.cluster;
     for (int r = rank * kThreads + tid; r < ntake; r += stride) {
         const int b = last_le(s_first, P.B, r);               // the request that takes page r (ties: the last, which takes)
-        P.table[(int64_t)b * P.max_pages + s_held[b] + r - s_first[b]] = P.free_pages[count - 1 - r];
+        const int page = P.free_pages[count - 1 - r];
+        if (page < 0 || page >= P.num_pages) set_status(P.status, DSPARK_DEV_BAD_PAGE);       // (its tokens, if any, get no slot below)
+        P.table[(int64_t)b * P.max_pages + s_held[b] + r - s_first[b]] = page;
     }
     // four neighbouring tokens a thread: one search, their pages fetched together
     for (int t0 = (rank * kThreads + tid) * kTok; t0 < P.max_tokens; t0 += stride * kTok) {

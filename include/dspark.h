@@ -427,9 +427,9 @@ typedef struct dspark_paged_cache {
  * anything is taken: a negative number, a request past max_pages, more new tokens
  * than max_tokens or more pages than are free refuse the whole call, with
  * DSPARK_DEV_CAPACITY in the cache's status: cu_new is then 0 throughout, every
- * slot -1, kv_len = ctx_len, and pages, counts and tables stay as they were. A page number outside
- * [0, num_pages) sets DSPARK_DEV_BAD_PAGE and gives its tokens slot -1. cache.k
- * and cache.v are not read. B <= 4096, max_tokens <= 2^30.
+ * slot -1, kv_len = ctx_len, and pages, counts and tables stay as they were. The number of a page taken, or of
+ * one that a new token falls into, outside [0, num_pages) sets DSPARK_DEV_BAD_PAGE and gives its tokens slot -1. cache.k
+ * and cache.v are not read. 1 <= B <= 4096 (and cache.batch), max_tokens <= 2^30.
  */
 int dspark_page_slots(const dspark_paged_cache* cache, const int32_t* ctx_len, const int32_t* n_new, int32_t B,
                       const int32_t* n_pages, const int32_t* free_pages, int32_t n_free, const int32_t* free_count,

@@ -154,3 +154,12 @@ def test_tables_around_the_default_shared_memory(B):
             "assert cu.tolist() == list(range(B + 1)) and slots.tolist() == [16 * (B - 1 - i) for i in range(B)] and int(count) == 0\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_page_slots_bad_page_without_a_new_token_is_reported():
+    """Pages that a request takes for rows it has cached already: a number outside the pool is reported too."""
+    import block_draft_model_dspark_b200 as dsp
+    cache = cache_of(np.full((1, 3), -1, np.int32), 10, 16)
+    cu, kv, slots, pos, held, count = dsp.page_slots(cache, dev([40]), dev([1]), dev([0]), dev([2, 5, 77]), dev([3]), 4)
+    assert held.tolist() == [3] and count.tolist() == [0] and slots.tolist() == [2 * 16 + 8, -1, -1, -1]
+    assert cache.read_status() == dsp.DSPARK_DEV_BAD_PAGE
