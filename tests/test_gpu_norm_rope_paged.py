@@ -114,3 +114,37 @@ def test_norm_rope_no_tokens():
     out = dsp.norm_rope_paged(z, z, z, None, None, dsp.rope_inv_freq(64), torch.zeros(0, dtype=torch.int32, device="cuda"),
                               torch.zeros(0, dtype=torch.int64, device="cuda"), cache, 0)
     assert out.shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("x,kv", [("bf16", "bf16"), ("fp32", "fp16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("T,nH,nKv,hd", [(1200, 32, 8, 128), (1201, 33, 1, 48), (1190, 16, 2, 256), (601, 33, 3, 192), (301, 70, 5, 64), (2400, 7, 7, 16)])
+def test_several_rounds_of_heads_a_warp(x, kv, T, nH, nKv, hd):
+    """Prompt chunks: a warp has more heads than it takes at a time (one warp per token from 1184 tokens on, several below)."""
+    import block_draft_model_dspark_b200 as dsp
+    g = torch.Generator().manual_seed(T + hd)
+    xt, kt, page = DT[x], DT[kv], 16
+    qkv = (torch.randn(T, (nH + 2 * nKv) * hd, generator=g) * 2).to(xt).cuda()
+    q, k, v = (t.unflatten(1, (-1, hd)) for t in qkv.split([nH * hd, nKv * hd, nKv * hd], 1))
+    qn, kn = ((1 + 0.2 * torch.randn(hd, generator=g)).to(xt).cuda() for _ in range(2))
+    freq = dsp.rope_inv_freq(hd, 1e4)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g).to(torch.int32).cuda()
+    pages = T // page + 2
+    slots = torch.randperm(pages * page, generator=g)[:T].clone()
+    slots[::7] = -1
+    for v_norm in (True, False):
+        kc, vc = (torch.full((1, pages, page, nKv, hd), 7.0, dtype=kt, device="cuda") for _ in range(2))
+        cache = dsp.PagedKvCache(pages, page, nKv, hd, block_table=torch.zeros(1, 1, dtype=torch.int32, device="cuda"), k=kc, v=vc)
+        out = torch.full((T, nH, hd), 5.0, dtype=kt, device="cuda")
+        dsp.norm_rope_paged(q, k, v, qn, kn, freq, pos, slots.cuda(), cache, 0, eps=1e-5, v_norm=v_norm, q_out=out)
+        real, at = slots >= 0, slots[slots >= 0]
+        rest = torch.ones(pages * page, dtype=torch.bool)
+        rest[at] = False
+        assert bool((out.cpu()[~real] == 5.0).all())
+        y, mag = ref_heads(q, qn, 1e-5, True, pos, freq)
+        check(out.cpu()[real], y[real], mag[real], hd, kt, "q")
+        for c, src, gain, norm, f, what in ((kc, k, kn, True, freq, "k"), (vc, v, None, v_norm, None, "v")):
+            y, mag = ref_heads(src, gain, 1e-5, norm, pos, f)
+            rows = c[0].flatten(0, 1).cpu()
+            check(rows[at], y[real], mag[real], hd, kt, what)
+            assert bool((rows[rest] == 7.0).all())
+        assert cache.read_status() == 0
