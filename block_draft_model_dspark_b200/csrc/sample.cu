@@ -47,6 +47,8 @@ constexpr int kWarps = NT / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 4096;
 constexpr int kMaxCluster = 16;
+constexpr int kPlaces = 1024;                        // steps of a place within a bin
+constexpr int kSliceMax = (int)(0xffffffffu / (kPlaces - 1));         // 4.2 million entries
 constexpr float kPerUnit = 64.f;                     // bins per unit of (m - x) / T
 constexpr size_t kHeadBytes = kList * 8;             // the histogram, later the list
 constexpr double kSlack = 3e-5;                      // above the relative rounding of a bin and its edge's weight (32 bits, (m - x) / T up to 32)
@@ -54,7 +56,6 @@ constexpr double kFixed = 2251799813685248.0;        // 2^51: sums of kList weig
 
 struct SampleParams {
     const void* logits; int64_t stride; int rows, V, cluster, slice, resident;
-    float places;                                    // steps of a place within a bin: a slice's places add up to less than 2^32
     const float* u; const float* temperature; const int32_t* top_k; const float* top_p; const float* min_p;
     int32_t* tokens; float* probs;
 };
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
     using Heavy = std::integral_constant<int, 2>;             // and those that sum weights
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);       // [kBins] elements
-    uint32_t* place = hist + kBins;                           // [kBins] their places in the bin, in 1/places; then the mean as a float
+    uint32_t* place = hist + kBins;                           // [kBins] their places in the bin, in 1 / kPlaces; then the mean as a float
     uint64_t* list = reinterpret_cast<uint64_t*>(smem);
     uint4* data = reinterpret_cast<uint4*>(smem + kHeadBytes);
     __shared__ Scratch S;
@@ -547,15 +548,14 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
             const float z = W.z(x);
             const int b = min((int)z, kBins - 1);
             atomicAdd(&hist[b], 1u);
-            atomicAdd(&place[b], min((uint32_t)((z - (float)b) * P.places), (uint32_t)P.places - 1));
+            atomicAdd(&place[b], min((uint32_t)((z - (float)b) * kPlaces), kPlaces - 1u));
         });
         meet();
         const double total = sum_of(S.x.total), target = (double)p * total;
         // sums of the rank's share of the bins over the cluster
         const int nb = kBins / C;
-        const float step = 1.f / P.places;                    // (a place is rounded down)
         auto lower = [&](int b, uint32_t n, float mean) {     // bounds of a bin's mass
-            return b == kBins - 1 ? 0.0 : (double)n * (1.0 - kSlack) * __expf(-((float)b + mean + step) * (1.f / kPerUnit));
+            return b == kBins - 1 ? 0.0 : (double)n * (1.0 - kSlack) * __expf(-((float)b + mean + 1.f / kPlaces) * (1.f / kPerUnit));
         };
         auto upper = [&](int b, uint32_t n, float mean) {     // (the last bin has no end)
             return (double)n * (1.0 + kSlack) * 1.000031 * __expf(-((float)b + (b == kBins - 1 ? 0.f : mean)) * (1.f / kPerUnit));
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleParams P) {
                 at += get_u32(&place[b], q);
             }
             hist[b] = c;                                      // no other rank reads this rank's share before the next meeting
-            place[b] = __float_as_uint(c > 0 ? (float)(at / ((double)P.places * c)) : 0.f);
+            place[b] = __float_as_uint(c > 0 ? (float)(at / ((double)kPlaces * c)) : 0.f);
         }
         meet();
         constexpr int PER = kBins / NT;                       // every CTA has all bins, a few a thread
@@ -810,14 +810,12 @@ template <typename X>
 cudaError_t launch(SampleParams P, cudaStream_t s) {
     constexpr int VEC = 16 / (int)sizeof(X);
     auto slice = [&](int c) { return (int)(((int64_t)P.V + VEC - 1 + c - 1) / c + VEC - 1) / VEC * VEC; };
-    // Rows are split while they leave SMs idle (148, two CTAs each) and a slice is long enough to pay for the exchanges.
+    // Rows are split while they leave SMs idle (148, two CTAs each) and a slice is long enough to pay for the exchanges;
+    // and, whatever their number, down to slices whose places in one bin add up in 32 bits (four CTAs for 2^24 entries).
     int c = 1;
-    while (c < kMaxCluster && (int64_t)P.rows * c * 2 <= 296 && slice(c) > 4096) c *= 2;
+    while (c < kMaxCluster && (((int64_t)P.rows * c * 2 <= 296 && slice(c) > 4096) || slice(c) > kSliceMax)) c *= 2;
     P.cluster = c;
     P.slice = slice(c);
-    // 1024 steps (a 2^-16th of a weight) up to 4.2 million entries a slice, 256 for the largest
-    P.places = 1024.f;
-    while ((int64_t)P.slice * ((int64_t)P.places - 1) >= (int64_t)1 << 32) P.places *= 0.5f;
     // Shared memory for two CTAs an SM, or for one where there are no more CTAs than SMs.
     const size_t room = ((int64_t)P.rows * c <= 148 ? 208 * 1024 : 104 * 1024) - kHeadBytes;
     P.resident = P.slice * sizeof(X) <= room;

@@ -194,12 +194,12 @@ def test_streamed_rows_on_dirty_shared_memory():
             assert torch.equal(probs, share)
 
 
-@pytest.mark.parametrize("dt,V,near,below", [("fp32", 5_100_001, 4_330_000, 0.98 / 64), ("fp16", (1 << 24) - 1, 15_500_000, 9 * 2.0 ** -11)])
+@pytest.mark.parametrize("dt,V,near,below", [("fp32", 4_198_401, 4_100_000, 0.998 / 64), ("fp32", 5_100_001, 4_330_000, 0.98 / 64), ("fp16", (1 << 24) - 1, 15_500_000, 9 * 2.0 ** -11)])
 def test_millions_of_logits_in_one_bin(dt, V, near, below):
-    """One CTA's share of top-p's histogram with millions of entries in the maximum's bin, `below` the maximum, where
-    their places (in 1 / 1024 of a bin) add up to more than 2^32, and a thin tail in which the prefix ends."""
+    """Top-p's histogram with millions of entries in the maximum's bin, `below` the maximum, whose places (in 1 / 1024 of a
+    bin) come close to 2^32 together or pass it, and a thin tail in which the prefix ends."""
     import block_draft_model_dspark_b200 as dsp
-    R = 150                                                       # more than half the places: a CTA per row
+    R = 150                                                       # as few CTAs a row as their slices allow: one, two, four
     rng = np.random.default_rng(V)
     x = torch.empty(V)
     x[:near] = 1.0 - below
