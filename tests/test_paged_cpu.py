@@ -1,7 +1,10 @@
 """The paged verification step's C entry points without a GPU: every refusal returns its code, with a message,
 before anything is launched (the pointers here are numbers that nothing may touch)."""
 import ctypes
+import os
+import re
 
+import numpy as np
 import pytest
 
 P = 4096            # an aligned address that is never read
@@ -167,3 +170,21 @@ def test_packed_integers_past_32_bits_are_refused(dsp):
                 words = struct.pack("@" + "".join("d" if isinstance(a, float) else "q" for a in bad), *bad)
                 refused(dsp, lib.dspark_packed_call(call, words), -1)
                 assert b"32 bits" in lib.dspark_last_error(), (call, i, far, lib.dspark_last_error())
+
+
+def test_attention_polynomial_is_as_close_as_its_comment_says():
+    """2^f on |f| <= 1/2 by the kernel's coefficients, in fp32 with fused multiply-adds: within 2^-22."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "block_draft_model_dspark_b200", "csrc", "attend_paged_tc.cu")) as f:
+        body = re.search(r"void exp2_poly\(.*?\n}", f.read(), re.S).group(0)
+    pair = r"f2\(([\d.e-]+)f, \1f\)"
+    first = re.search(r"fma2\(" + pair + r", f, " + pair.replace("\\1", "\\2") + r"\)", body)
+    rest = re.findall(r"p = fma2\(p, f, " + pair + r"\)", body)
+    c = [np.float32(v) for v in list(first.groups()) + rest]
+    assert len(c) == 6
+    x = np.linspace(-0.5, 0.5, 1 << 20).astype(np.float32)
+    p = np.full_like(x, c[0])
+    for k in c[1:]:                                       # a product of two fp32 is exact in 64 bits, the sum far more exact than fp32
+        p = (p.astype(np.float64) * x.astype(np.float64) + np.float64(k)).astype(np.float32)
+    t = np.exp2(x.astype(np.float64))
+    assert np.abs(p.astype(np.float64) / t - 1).max() < 2.0 ** -22
