@@ -307,7 +307,8 @@ class PagedKvCache:
 
     ``k``, ``v`` and ``block_table`` may be given (the caller's tensors, which must stay alive and in
     place) or are allocated: ``batch`` and ``max_pages`` then size the table (-1 throughout).
-    ``read_status()`` returns and clears the ``DSPARK_DEV_*`` bits the kernels recorded."""
+    ``read_status()`` returns and clears the ``DSPARK_DEV_*`` bits the kernels recorded (it waits for the current stream:
+    work on another one is to be waited for first)."""
 
     def __init__(self, num_pages: int, page_size: int, n_kv: int, head_dim: int, block_table=None, batch: int = 0,
                  max_pages: int = 0, layers: int = 1, dtype=None, device="cuda", k=None, v=None):
@@ -419,7 +420,7 @@ def norm_rope_paged(q, k, v, q_norm, k_norm, inv_freq, positions, slots, cache: 
 
 def rope_inv_freq(head_dim: int, theta: float = 1e6, partial_rotary_factor: float = 1.0, device="cuda"):
     """The proportional RoPE table [head_dim / 2] in float64: theta^(-2i / head_dim) for the first
-    floor(head_dim * partial) / 2 pairs, 0 (identity) for the rest."""
+    floor(head_dim * partial) / 2 pairs, 0 (identity) for the rest. Made on the host and copied: once per model, not per call."""
     import torch
     i = torch.arange(head_dim // 2, dtype=torch.float64)
     f = float(theta) ** (-2.0 * i / head_dim)
@@ -464,7 +465,7 @@ def attend_paged(q, cache: PagedKvCache, layer: int, cu_new, kv_len, max_new: in
 
 
 def sample_workspace(rows: int, vocab: int, device="cuda", stream=None):
-    """A workspace for ``sample`` calls of up to this many rows and entries."""
+    """A workspace for ``sample`` calls of up to this many rows and entries (checked, not written: calls may share one)."""
     import torch
     return _empty(max(int(get_lib().dspark_sample_workspace_bytes(rows, vocab)), 256), torch.uint8, device, stream)
 

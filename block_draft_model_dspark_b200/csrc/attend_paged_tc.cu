@@ -14,11 +14,14 @@
 // The running maximum m is raised only when a tile's exceeds it by 8 (log2), so O
 // is rarely rescaled; P stays below 256.
 //
-// Bound by the K and V bytes for few new tokens (64 requests of 8K to 32K keys, one token each: 852 us, 6.05 TB/s; 6.6
-// with pages of 64), by the chain S -> softmax -> PV for prompt chunks (4 x 2048 tokens over up to 8K keys, head_dim 128:
-// 450 us, 1000 TFLOP/s, tensor pipe 53% active), by the loads for head_dim 256, whose tiles serve 128 rows only
-// (8191 tokens in a window of 1024: 182 us, 750 TFLOP/s; without the window 990). One request's 17 tokens over 4096
-// keys take 22 us: two launches, and a few microseconds each for finding the share, the first tile and the pieces' join.
+// Bound by the K and V bytes for few new tokens (64 requests of 8K to 32K keys, one token each: 860 us in a short run, 6.0
+// TB/s, 925 to 1000 in a long one, by the GPU; 745 with pages of 64; head_dim 64 moves 32 KB a step and stays at 3.4 to 4.4
+// TB/s), by the chain S -> softmax -> PV for prompt chunks (4 x 2048 tokens over up to 8K keys, head_dim 128: 450 us,
+// 1000 TFLOP/s, tensor pipe 53% active; 510 to 520 us in a long run, at the power limit's clocks). head_dim 256 has the
+// same chain with one query tile and 64 keys a step (8191 tokens in a window of 1024: 185 us, 200 in a long run, tensor pipe 43%, L2
+// at 27% of its rate; units of 17 tiles pay their start and epilogue too: 690 to 750 TFLOP/s, 900 without the window). One
+// request's 17 tokens over 4096 keys take 21 us: two launches, and a few microseconds each for finding the share, the
+// first tile and the pieces' join.
 //
 // Steps: with NQ = 2 (prompt chunks, head_dim <= 128, KT = 128) step s is tile s / 2 of
 // query tile s % 2, with NQ = 1 it is tile s; step s uses S buffer s % 2. The

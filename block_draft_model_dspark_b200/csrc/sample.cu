@@ -30,8 +30,9 @@
 // of them share a bank) times the Taylor polynomial of degree 6 on |r| <= 1/32 octave, within
 // 2^-46: 12 64-bit operations an element.
 //
-// 512 rows of 262144 fp32 logits: greedy 135 us (4.0 TB/s), top-k 228 us (two passes over the row), unfiltered 288 us
-// (the 64-bit operations), top-p 480 to 790 us (a third and a fourth pass, or a fifth far down the tail). One such row:
+// 512 rows of 262144 fp32 logits: greedy 135 us (4.0 TB/s; 512 CTAs on 296 places), top-k 228 us (two passes over the row),
+// unfiltered 290 us (issue slots 63%, 64-bit pipe 42%), top-p 480 to 790 us (a third and a fourth pass, or a fifth far
+// down the tail). One such row:
 // 8 to 42 us, the exchanges of its 16 CTAs.
 #include <cfloat>
 #include <type_traits>

@@ -499,7 +499,7 @@ int dspark_attend_paged(const dspark_paged_cache* cache, int32_t layer, const vo
  * temperature T <= 0: the largest logit (lowest index on ties). Else, with weights
  * w_i = exp((x_i - max x) / T) and the candidates in falling order (equal logits: the lower
  * index first): top_k > 0 keeps the first top_k; top_p < 1, of those, the shortest prefix
- * whose weight reaches top_p of theirs (at least one); min_p > 0 those with w_i >=
+ * whose weight reaches top_p of theirs (at least one); min_p > 0 the first and those with w_i >=
  * min_p. The token is the first i, in the vocabulary's order, whose cumulative kept
  * weight exceeds u times the kept total (the last kept one where u >= 1).
  *   logits  device T [rows][vocab], T = dtype, row_stride elements between rows; a NaN counts as -infinity
@@ -508,8 +508,8 @@ int dspark_attend_paged(const dspark_paged_cache* cache, int32_t layer, const vo
  *           NULL (1, 1, 0 and 0: not filtered)
  *   tokens  device int32 [rows]; -1 for a row without a logit above -infinity
  *   probs   device float [rows] or NULL: the token's share of the kept weight
- *   ws      >= dspark_sample_workspace_bytes(rows, vocab), 256-byte aligned; calls that may
- *           overlap on the GPU need one each
+ *   ws      >= dspark_sample_workspace_bytes(rows, vocab), 256-byte aligned. It is checked only: what a row needs
+ *           is held in shared memory, so any calls may share one
  * Weights are within 2^-45 and summed in 64 bits; one below 2^-79 of the largest counts as 0 (such a
  * candidate is not drawn). vocab <= 2^24, rows <= 2^26.
  */

@@ -141,7 +141,7 @@ def test_many_tokens_over_a_cluster():
         assert cache.read_status() == 0
 
 
-@pytest.mark.parametrize("B", [3055, 3056, 3071, 3072])
+@pytest.mark.parametrize("B", [3055, 3056, 3071, 3080])
 def test_tables_around_the_default_shared_memory(B):
     """The largest batches that fit it and the first that do not, each as the first call of a process (the opt-in to more
     stays with the kernel once it is made)."""
@@ -163,3 +163,26 @@ def test_page_slots_bad_page_without_a_new_token_is_reported():
     cu, kv, slots, pos, held, count = dsp.page_slots(cache, dev([40]), dev([1]), dev([0]), dev([2, 5, 77]), dev([3]), 4)
     assert held.tolist() == [3] and count.tolist() == [0] and slots.tolist() == [2 * 16 + 8, -1, -1, -1]
     assert cache.read_status() == dsp.DSPARK_DEV_BAD_PAGE
+
+
+def test_pages_of_finished_requests_come_back():
+    """Requests that end push their pages onto the free stack: every page belongs to one request or to the stack."""
+    import block_draft_model_dspark_b200 as dsp
+    rng = np.random.default_rng(50)
+    B, pages = 6, 60
+    cache = dsp.PagedKvCache(pages, 16, 1, 16, batch=B, max_pages=30)
+    free, count = torch.from_numpy(rng.permutation(pages).astype(np.int32)).cuda(), dev([pages])
+    ctx, held = dev([0] * B), dev([0] * B)
+    for step in range(12):
+        new = dev(rng.integers(0, 40, B).tolist())
+        dsp.page_slots(cache, ctx, new, held, free, count, 40 * B, n_pages_out=held, free_count_out=count, kv_len=ctx)
+        assert cache.read_status() == 0
+        ctx -= torch.minimum(new, dev(rng.integers(0, 5, B).tolist()))
+        b = int(torch.argmax(ctx))                                # the longest ends
+        n, c = int(held[b]), int(count)
+        free[c:c + n] = cache.block_table[b, :n]
+        count += n
+        held[b] = 0
+        ctx[b] = 0
+        owned = [int(p) for i in range(B) for p in cache.block_table[i, :int(held[i])]]
+        assert sorted(owned + free[:int(count)].tolist()) == list(range(pages))
